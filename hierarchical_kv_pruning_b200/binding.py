@@ -25,6 +25,7 @@ ATLASKV_F32, ATLASKV_BF16 = 0, 1
 ATLASKV_LEAVES_DEVICE, ATLASKV_LEAVES_HOST_PINNED = 0, 1
 ATLASKV_PROFILE_TIMES, ATLASKV_PROFILE_COUNTERS = 1, 2
 ATLASKV_DESCENT_AUTO, ATLASKV_DESCENT_FUSED, ATLASKV_DESCENT_PARENT_MAJOR = 0, 1, 2
+ATLASKV_ROPE_HALF, ATLASKV_ROPE_INTERLEAVED = 0, 1
 STAGE_NAMES = ("descend", "staging", "attend", "attend_seq", "attend_leaf")
 
 # Every symbol include/atlaskv.h declares.
@@ -32,7 +33,10 @@ EXPORTED = ("atlaskv_create_tree", "atlaskv_workspace_size", "atlaskv_attend", "
             "atlaskv_set_profiling", "atlaskv_stage_times", "atlaskv_refine_stats", "atlaskv_attend_static",
             "atlaskv_probe_wait_timeout", "atlaskv_destroy", "atlaskv_last_error", "atlaskv_workspace_size_layers",
             "atlaskv_attend_layers", "atlaskv_create_tree_csr", "atlaskv_workspace_size_csr", "atlaskv_attend_csr",
-            "atlaskv_set_descent", "atlaskv_set_leaf_cache", "atlaskv_leaf_cache_stats")
+            "atlaskv_set_descent", "atlaskv_set_leaf_cache", "atlaskv_leaf_cache_stats", "atlaskv_rope_init",
+            "atlaskv_rope", "atlaskv_cache_page_bytes", "atlaskv_create_cache", "atlaskv_destroy_cache",
+            "atlaskv_cache_sync_status", "atlaskv_cache_append", "atlaskv_cache_read", "atlaskv_cache_workspace_size",
+            "atlaskv_cache_attend")
 MAX_LAYERS = 32
 MAX_LEVELS = 4
 # Size of the library's static device scratch (ATLASKV_STATIC_SCRATCH_BYTES).
@@ -94,6 +98,44 @@ class atlaskv_io(ctypes.Structure):
     ]
 
 
+class atlaskv_rope_spec(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("freq", ctypes.c_double * 64)]
+
+
+class atlaskv_rope_io(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("H", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("tokens", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("positions", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("y_stride", ctypes.c_int64), ("backward", ctypes.c_int32),
+    ]
+
+
+class atlaskv_cache_desc(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("pages", ctypes.c_void_p)]
+
+
+class atlaskv_seqs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_len", ctypes.c_void_p)]
+
+
+class atlaskv_append_io(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64), ("positions", ctypes.c_void_p), ("H", ctypes.c_int32), ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+    ]
+
+
+class atlaskv_cache_attend_io(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("H", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -131,6 +173,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             lib.atlaskv_refine_stats.argtypes = [V, ctypes.POINTER(ctypes.c_uint64), I32]
             lib.atlaskv_probe_wait_timeout.argtypes = [V, V]
             lib.atlaskv_destroy.argtypes = [V]
+            F64, SEQS = ctypes.c_double, ctypes.POINTER(atlaskv_seqs)
+            lib.atlaskv_rope_init.argtypes = [ctypes.POINTER(atlaskv_rope_spec), I32, I32, F64, F64, F64, F64, F64,
+                                              ctypes.c_float]
+            lib.atlaskv_rope.argtypes = [ctypes.POINTER(atlaskv_rope_spec), ctypes.POINTER(atlaskv_rope_io), V]
+            lib.atlaskv_cache_page_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
+            lib.atlaskv_create_cache.argtypes = [ctypes.POINTER(atlaskv_cache_desc), V, ctypes.POINTER(V)]
+            lib.atlaskv_destroy_cache.argtypes = [V]
+            lib.atlaskv_cache_sync_status.argtypes = [V, V]
+            lib.atlaskv_cache_append.argtypes = [V, ctypes.POINTER(atlaskv_rope_spec), SEQS,
+                                                 ctypes.POINTER(atlaskv_append_io), V]
+            lib.atlaskv_cache_read.argtypes = [V, SEQS, I32, V, V, V]
+            lib.atlaskv_cache_workspace_size.argtypes = [V, I32, I32, I32, I32, ctypes.POINTER(SZ)]
+            lib.atlaskv_cache_attend.argtypes = [V, SEQS, ctypes.POINTER(atlaskv_cache_attend_io), V, SZ, V]
             lib.atlaskv_last_error.argtypes = []
             lib.atlaskv_last_error.restype = ctypes.c_char_p
             for name in EXPORTED:
@@ -267,6 +322,61 @@ def atlaskv_probe_wait_timeout(tree: int, stream: int = 0) -> None:
 
 def atlaskv_destroy(tree: int) -> None:
     _check(load_library().atlaskv_destroy(ctypes.c_void_p(tree)))
+
+
+def atlaskv_rope_init(layout: int, rotary_dim: int, base: float, factor: float, original_len: float,
+                      low_turns: float, high_turns: float, amplitude: float) -> atlaskv_rope_spec:
+    spec = atlaskv_rope_spec()
+    _check(load_library().atlaskv_rope_init(ctypes.byref(spec), layout, rotary_dim, base, factor, original_len,
+                                            low_turns, high_turns, amplitude))
+    return spec
+
+
+def atlaskv_rope(spec: atlaskv_rope_spec, io: atlaskv_rope_io, stream: int = 0) -> None:
+    _check(load_library().atlaskv_rope(ctypes.byref(spec), ctypes.byref(io), stream))
+
+
+def atlaskv_cache_page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().atlaskv_cache_page_bytes(n_kv_heads, head_dim, page_size, ctypes.byref(out)))
+    return out.value
+
+
+def atlaskv_create_cache(desc: atlaskv_cache_desc, stream: int = 0) -> int:
+    handle = ctypes.c_void_p()
+    _check(load_library().atlaskv_create_cache(ctypes.byref(desc), stream, ctypes.byref(handle)))
+    return handle.value
+
+
+def atlaskv_destroy_cache(cache: int) -> None:
+    _check(load_library().atlaskv_destroy_cache(cache))
+
+
+def atlaskv_cache_sync_status(cache: int, stream: int = 0) -> None:
+    _check(load_library().atlaskv_cache_sync_status(cache, stream))
+
+
+def atlaskv_cache_append(cache: int, rope: Optional[atlaskv_rope_spec], seqs: atlaskv_seqs, io: atlaskv_append_io,
+                         stream: int = 0) -> None:
+    _check(load_library().atlaskv_cache_append(cache, None if rope is None else ctypes.byref(rope), ctypes.byref(seqs),
+                                               ctypes.byref(io), stream))
+
+
+def atlaskv_cache_read(cache: int, seqs: atlaskv_seqs, dtype: int, k_out: Optional[int], v_out: Optional[int],
+                       stream: int = 0) -> None:
+    _check(load_library().atlaskv_cache_read(cache, ctypes.byref(seqs), dtype, k_out, v_out, stream))
+
+
+def atlaskv_cache_workspace_size(cache: int, dtype: int, B: int, N: int, H: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().atlaskv_cache_workspace_size(cache, dtype, B, N, H, ctypes.byref(out)))
+    return out.value
+
+
+def atlaskv_cache_attend(cache: int, seqs: atlaskv_seqs, io: atlaskv_cache_attend_io, workspace: Optional[int],
+                         workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().atlaskv_cache_attend(cache, ctypes.byref(seqs), ctypes.byref(io), workspace,
+                                               workspace_bytes, stream))
 
 
 # ---- torch-facing convenience ------------------------------------------------
@@ -518,3 +628,210 @@ class CsrHikvpTree:
 
     def refine_stats(self):
         return atlaskv_refine_stats(self.handle)
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype):
+    """(pointer, token stride) of a token tensor [B][N][heads][D] whose token
+    rows are dense and evenly spaced, as a slice of a wider projection's is."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise AtlaskvError(ATLASKV_EINVAL, "%s: %s of shape %s, expected %s of shape %s" %
+                           (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), shape[2] * shape[3]
+    s0, s1, s2, s3 = t.stride()
+    if shape[1] == 1:      # one token per sequence: the stride between sequences is the token stride
+        s1 = s0
+    if shape[0] * shape[1] == 1:
+        s1 = shape[2] * shape[3]
+    if s3 != 1 or (s2 != shape[3] and shape[2] > 1) or (shape[0] > 1 and s0 != shape[1] * s1):
+        raise AtlaskvError(ATLASKV_EINVAL, "%s: its tokens must be dense rows at an even stride" % name)
+    return t.data_ptr(), s1
+
+
+def _dense(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise AtlaskvError(ATLASKV_EINVAL, "%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
+    return t.data_ptr()
+
+
+def _ints(name: str, t: Optional[torch.Tensor], shape) -> Optional[int]:
+    return None if t is None else _dense(name, t, shape, torch.int32)
+
+
+def _on_device(device: torch.device, tensors, stream) -> int:
+    """The stream to launch on: `stream`, or the current one of the current
+    device, where every tensor has to be."""
+    if device.index != torch.cuda.current_device():
+        raise AtlaskvError(ATLASKV_EINVAL, "%s is not the current device" % device)
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise AtlaskvError(ATLASKV_EINVAL, "a tensor on %s in a call on %s" % (t.device, device))
+    return _stream(stream)
+
+
+def _used_on(stream, *tensors):
+    """Outputs allocated here belong to the current stream; a call on another one uses them there."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+class Rope:
+    """Rotary positions: frequencies base^(-2 i / rotary_dim), rescaled for
+    contexts `factor` times original_len (see atlaskv_rope_init)."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
+                 original_len: float = 0, low_turns: float = 1.0, high_turns: float = 32.0, amplitude: float = 1.0):
+        self.spec = atlaskv_rope_init(ATLASKV_ROPE_INTERLEAVED if interleaved else ATLASKV_ROPE_HALF, int(rotary_dim),
+                                      float(base), float(factor), float(original_len), float(low_turns),
+                                      float(high_turns), float(amplitude))
+
+
+def rope(x, positions, spec: Rope, out=None, backward: bool = False, stream=None):
+    """Rotate x [B][N][H][D] by positions [B][N] (int32) into out (a new
+    tensor by default; x itself for in place).  backward=True is the transpose:
+    it turns a gradient of the rotated tensor into that of the tensor."""
+    if x.dim() != 4:
+        raise AtlaskvError(ATLASKV_EINVAL, "x must be [B][N][H][D]")
+    shape, given = x.shape, out
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    s = _on_device(x.device, (positions, out), stream)
+    xp, xs = _rows("x", x, shape, x.dtype)
+    yp, ys = _rows("out", out, shape, x.dtype)
+    io = atlaskv_rope_io(_dtype_code(x.dtype), shape[2], shape[3], shape[0] * shape[1], xp, xs,
+                         _ints("positions", positions, shape[:2]), yp, ys, 1 if backward else 0)
+    atlaskv_rope(spec.spec, io, s)
+    if given is None:
+        _used_on(stream, out)
+    return out
+
+
+class KvCache:
+    """A pool of 4-bit cache pages registered with the library.  pages: uint8
+    [n_pages][page bytes] on the GPU (KvCache.page_bytes gives the width),
+    borrowed and kept alive.  The calls take one batch's block_table
+    [B][max_pages], kv_len [B] and q_len [B] (or None: every row), int32 on the
+    GPU, as atlaskv_seqs describes them; a decode step appends its tokens and
+    attends with the same three."""
+
+    def __init__(self, pages, n_kv_heads: int, head_dim: int, page_size: int, stream=None):
+        self.handle = None
+        self.n_kv_heads, self.head_dim, self.page_size = int(n_kv_heads), int(head_dim), int(page_size)
+        width = self.page_bytes(n_kv_heads, head_dim, page_size)
+        if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != width or not pages.is_cuda:
+            raise AtlaskvError(ATLASKV_EINVAL, "pages must be a uint8 [n_pages][%d] CUDA tensor" % width)
+        self.pages, self.device = pages, pages.device
+        d = atlaskv_cache_desc(self.n_kv_heads, self.head_dim, self.page_size, pages.shape[0], _ptr(pages))
+        self.handle = atlaskv_create_cache(d, _on_device(self.device, (), stream))
+
+    @staticmethod
+    def page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
+        return atlaskv_cache_page_bytes(int(n_kv_heads), int(head_dim), int(page_size))
+
+    @classmethod
+    def allocate(cls, n_pages: int, n_kv_heads: int, head_dim: int, page_size: int, device="cuda", stream=None):
+        pages = torch.empty((int(n_pages), cls.page_bytes(n_kv_heads, head_dim, page_size)), dtype=torch.uint8,
+                            device=device)
+        return cls(pages, n_kv_heads, head_dim, page_size, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            atlaskv_destroy_cache(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _seqs(self, N: int, block_table, kv_len, q_len) -> atlaskv_seqs:
+        B, width = block_table.shape
+        return atlaskv_seqs(B, N, width, _ints("block_table", block_table, (B, width)), _ints("kv_len", kv_len, (B,)),
+                            _ints("q_len", q_len, (B,)))
+
+    def append(self, k, v, block_table, kv_len, q_len=None, rope: Optional[Rope] = None, positions=None, q=None,
+               q_out=None, stream=None):
+        """Store the new tokens' k and v [B][N][H_kv][D] (k rotated when rope
+        is given, by positions [B][N] or by slot) and rotate the queries
+        q [B][N][H][D] into q_out along the way.  Returns q_out (None without q)."""
+        B, N = k.shape[:2]
+        given = q_out
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        s = _on_device(self.device, (k, v, block_table, kv_len, q_len, positions, q, q_out), stream)
+        shape = (B, N, self.n_kv_heads, self.head_dim)
+        kp, ks = _rows("k", k, shape, k.dtype)
+        vp, vs = _rows("v", v, shape, k.dtype)
+        qp, qs, H, qo = None, 0, 0, None
+        if q is not None:
+            H = q.shape[2] if q.dim() == 4 else 0
+            qp, qs = _rows("q", q, (B, N, H, self.head_dim), k.dtype)
+            qo = _dense("q_out", q_out, q.shape, k.dtype)
+        if block_table.shape[0] != B:
+            raise AtlaskvError(ATLASKV_EINVAL, "block_table has %d rows for %d sequences" % (block_table.shape[0], B))
+        io = atlaskv_append_io(_dtype_code(k.dtype), kp, vp, ks, vs, _ints("positions", positions, (B, N)), H, qp, qs,
+                               qo)
+        atlaskv_cache_append(self.handle, None if rope is None else rope.spec,
+                             self._seqs(N, block_table, kv_len, q_len), io, s)
+        if q is not None and given is None:
+            _used_on(stream, q_out)
+        return q_out
+
+    def read(self, N: int, block_table, kv_len, q_len=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+        """The q_len newest tokens of each sequence (q_len=kv_len: all of them)
+        as k, v [B][N][H_kv][D]; rows past q_len are left as they were (zero
+        in tensors allocated here)."""
+        shape = (block_table.shape[0], int(N), self.n_kv_heads, self.head_dim)
+        new = [k_out is None, v_out is None]
+        k_out = torch.zeros(shape, dtype=dtype, device=self.device) if k_out is None else k_out
+        v_out = torch.zeros(shape, dtype=k_out.dtype, device=self.device) if v_out is None else v_out
+        if stream is not None and any(new):   # the zeros were written on the current stream
+            stream.wait_stream(torch.cuda.current_stream())
+        s = _on_device(self.device, (block_table, kv_len, q_len, k_out, v_out), stream)
+        atlaskv_cache_read(self.handle, self._seqs(shape[1], block_table, kv_len, q_len), _dtype_code(k_out.dtype),
+                           _dense("k_out", k_out, shape, k_out.dtype), _dense("v_out", v_out, shape, k_out.dtype), s)
+        _used_on(stream, *[t for t, n in zip((k_out, v_out), new) if n])
+        return k_out, v_out
+
+    def workspace_size(self, dtype, B: int, N: int, H: int) -> int:
+        return atlaskv_cache_workspace_size(self.handle, _dtype_code(dtype), B, N, H)
+
+    def attend(self, q, block_table, kv_len, q_len=None, scale: float = 0.0, out=None, lse=None, workspace=None,
+               stream=None):
+        """Causal attention of q [B][N][H][D] over the stored sequences:
+        (out, lse).  Rows past q_len are left as they were."""
+        B, N, H, D = q.shape
+        new = []
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            new.append(out)
+        if lse is None:
+            lse = torch.empty((B, N, H), dtype=torch.float32, device=q.device)
+            new.append(lse)
+        code = _dtype_code(q.dtype)
+        if workspace is None:
+            nbytes = atlaskv_cache_workspace_size(self.handle, code, B, N, H)
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+            new.append(workspace)
+        s = _on_device(self.device, (q, block_table, kv_len, q_len, out, lse, workspace), stream)
+        qp, qs = _rows("q", q, (B, N, H, self.head_dim), q.dtype)
+        if block_table.shape[0] != B:
+            raise AtlaskvError(ATLASKV_EINVAL, "block_table has %d rows for %d sequences" % (block_table.shape[0], B))
+        io = atlaskv_cache_attend_io(code, H, qp, qs, _dense("out", out, (B, N, H, D), q.dtype),
+                                     _dense("lse", lse, (B, N, H), torch.float32), scale)
+        atlaskv_cache_attend(self.handle, self._seqs(N, block_table, kv_len, q_len), io, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), s)
+        _used_on(stream, *new)
+        return out, lse
+
+    def sync_status(self, stream=None):
+        """Raises on a device-side error of the calls so far."""
+        atlaskv_cache_sync_status(self.handle, _on_device(self.device, (), stream))

@@ -1,0 +1,430 @@
+// C ABI of the rotary positions and of the 4-bit paged cache (include/atlaskv.h):
+// argument checks and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+#include "atlaskv.h"
+#include "cache_attend.cuh"
+#include "internal.h"
+#include "kvcache.cuh"
+#include "rope.cuh"
+
+struct atlaskv_cache {
+    atlaskv_cache_desc d;
+    int device;
+    int num_sms;
+    int *status;   // device sticky status word
+};
+
+namespace {
+
+atlaskv_status fail(atlaskv_status st, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return akv_report(st, buf);
+}
+
+#define AKV_CUDA(call)                                                                                 \
+    do {                                                                                               \
+        cudaError_t e_ = (call);                                                                       \
+        if (e_ != cudaSuccess) {                                                                       \
+            cudaGetLastError();                                                                        \
+            return fail(ATLASKV_ECUDA, "%s: %s", #call, cudaGetErrorString(e_));                       \
+        }                                                                                              \
+    } while (0)
+#define AKV_RET(x)                                 \
+    do {                                           \
+        const atlaskv_status st_ = (x);            \
+        if (st_ != ATLASKV_OK) return st_;         \
+    } while (0)
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+int esize(int dtype) { return dtype == ATLASKV_F32 ? 4 : 2; }
+
+atlaskv_status check_dtype(int dtype)
+{
+    if (dtype != ATLASKV_F32 && dtype != ATLASKV_BF16) return fail(ATLASKV_EINVAL, "dtype %d", dtype);
+    return ATLASKV_OK;
+}
+
+atlaskv_status check_head_dim(int D)
+{
+    if (D != 64 && D != 128) return fail(ATLASKV_EUNSUPPORTED, "head_dim %d (64 or 128)", D);
+    return ATLASKV_OK;
+}
+
+// A token tensor: base aligned, stride 0 (dense) or at least a row and keeping
+// every row 16-byte aligned.  *stride becomes the stride in elements.
+atlaskv_status check_rows(const char *name, const void *p, int64_t row, int dtype, int64_t given, int64_t *stride)
+{
+    if (!p) return fail(ATLASKV_EINVAL, "null %s", name);
+    if (!aligned16(p)) return fail(ATLASKV_EINVAL, "%s must be 16-byte aligned", name);
+    if (given == 0) given = row;
+    if (given < row) return fail(ATLASKV_EINVAL, "%s: a token stride of %lld is below a row's %lld elements", name,
+                                 (long long)given, (long long)row);
+    if (given * esize(dtype) % 16) return fail(ATLASKV_EINVAL, "%s: its token stride must be a multiple of 16 bytes", name);
+    *stride = given;
+    return ATLASKV_OK;
+}
+
+atlaskv_status rope_params(const atlaskv_rope_spec *spec, int head_dim, akv::RopeParams *p)
+{
+    *p = akv::RopeParams{};
+    if (!spec) return ATLASKV_OK;
+    if (spec->layout != ATLASKV_ROPE_HALF && spec->layout != ATLASKV_ROPE_INTERLEAVED)
+        return fail(ATLASKV_EINVAL, "rotary layout %d", spec->layout);
+    if (spec->rotary_dim < 16 || spec->rotary_dim > head_dim || spec->rotary_dim % 16)
+        return fail(ATLASKV_EINVAL, "rotary_dim %d is not a multiple of 16 in [16, head_dim = %d]", spec->rotary_dim,
+                    head_dim);
+    if (!std::isfinite(spec->amplitude)) return fail(ATLASKV_EINVAL, "rotary amplitude is not finite");
+    p->on = 1;
+    p->interleaved = spec->layout == ATLASKV_ROPE_INTERLEAVED;
+    p->rot = spec->rotary_dim;
+    p->amp = spec->amplitude;
+    for (int i = 0; i < spec->rotary_dim / 2; ++i) {
+        if (!std::isfinite(spec->freq[i])) return fail(ATLASKV_EINVAL, "rotary frequency %d is not finite", i);
+        p->turns[i] = spec->freq[i] / (2.0 * 3.14159265358979323846);
+    }
+    return ATLASKV_OK;
+}
+
+atlaskv_status check_grid(long long blocks)
+{
+    if (blocks > 0x7fffffffLL) return fail(ATLASKV_EUNSUPPORTED, "too many tokens and heads for one launch");
+    return ATLASKV_OK;
+}
+
+int num_sms()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        n <= 0) {
+        cudaGetLastError();
+        n = 148;
+    }
+    return n;
+}
+
+// Rows per warp so that small calls spread over the device (one step of R
+// rows per warp) and large ones reuse a lane's cosines over many heads.
+int rows_per_warp(long long tokens, int rows, int R, int sms)
+{
+    const long long steps = tokens * ((rows + R - 1) / R);     // warps at one step each
+    const long long per = std::max(1LL, steps / ((long long)sms * 32));
+    return (int)std::min<long long>(per * R, (rows + R - 1) / R * R);
+}
+
+atlaskv_status check_cache(const atlaskv_cache *c)
+{
+    if (!c) return fail(ATLASKV_EINVAL, "null cache");
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ATLASKV_ECUDA, "no current CUDA device");
+    }
+    if (dev != c->device)
+        return fail(ATLASKV_EINVAL, "the cache lives on device %d and the current device is %d", c->device, dev);
+    return ATLASKV_OK;
+}
+
+atlaskv_status cache_params(const atlaskv_cache *c, const atlaskv_seqs *s, akv::CacheParams *p)
+{
+    if (!s) return fail(ATLASKV_EINVAL, "null seqs");
+    if (s->B < 0) return fail(ATLASKV_EINVAL, "B = %d < 0", s->B);
+    if (s->N < 1) return fail(ATLASKV_EINVAL, "N = %d < 1", s->N);
+    if (s->max_pages < 1) return fail(ATLASKV_EINVAL, "max_pages = %d < 1", s->max_pages);
+    if ((long long)s->max_pages * c->d.page_size > 0x7fffffffLL - 256)
+        return fail(ATLASKV_EUNSUPPORTED, "a block table of more than 2^31 slots");
+    *p = akv::CacheParams{};
+    p->pages = static_cast<uint8_t *>(c->d.pages);
+    p->n_pages = c->d.n_pages;
+    p->H_kv = c->d.n_kv_heads;
+    p->page_size = c->d.page_size;
+    p->B = s->B;
+    p->N = s->N;
+    p->max_pages = s->max_pages;
+    p->table = s->block_table;
+    p->kv_len = s->kv_len;
+    p->q_len = s->q_len;
+    p->status = c->status;
+    if (s->B == 0) return ATLASKV_OK;
+    if (!s->block_table || !s->kv_len) return fail(ATLASKV_EINVAL, "null block_table or kv_len");
+    if (!aligned4(s->block_table) || !aligned4(s->kv_len) || (s->q_len && !aligned4(s->q_len)))
+        return fail(ATLASKV_EINVAL, "block_table, kv_len and q_len must be 4-byte aligned");
+    return ATLASKV_OK;
+}
+
+// kernel<T, D>(args...) for the call's type and head dimension
+#define AKV_TD(dtype, D, LAUNCH)                                                     \
+    do {                                                                             \
+        if ((dtype) == ATLASKV_F32) {                                                \
+            if ((D) == 64) LAUNCH(float, 64);                                        \
+            else LAUNCH(float, 128);                                                 \
+        } else {                                                                     \
+            if ((D) == 64) LAUNCH(__nv_bfloat16, 64);                                \
+            else LAUNCH(__nv_bfloat16, 128);                                         \
+        }                                                                            \
+        AKV_CUDA(cudaGetLastError());                                                \
+    } while (0)
+
+}  // namespace
+
+extern "C" {
+
+atlaskv_status atlaskv_rope_init(atlaskv_rope_spec *spec, int32_t layout, int32_t rotary_dim, double base, double factor,
+                                 double original_len, double low_turns, double high_turns, float amplitude)
+{
+    if (!spec) return fail(ATLASKV_EINVAL, "null spec");
+    if (layout != ATLASKV_ROPE_HALF && layout != ATLASKV_ROPE_INTERLEAVED)
+        return fail(ATLASKV_EINVAL, "rotary layout %d", layout);
+    if (rotary_dim < 16 || rotary_dim > 2 * ATLASKV_ROPE_MAX_PAIRS || rotary_dim % 16)
+        return fail(ATLASKV_EINVAL, "rotary_dim %d is not a multiple of 16 in [16, %d]", rotary_dim,
+                    2 * ATLASKV_ROPE_MAX_PAIRS);
+    if (!(base > 0.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor) || !(original_len >= 0.0) ||
+        !std::isfinite(original_len) || !(low_turns >= 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns) ||
+        !std::isfinite(amplitude))
+        return fail(ATLASKV_EINVAL, "need base > 0, factor > 0, original_len >= 0, 0 <= low_turns < high_turns and a "
+                                    "finite amplitude");
+    atlaskv_rope_spec r = {};
+    r.layout = layout;
+    r.rotary_dim = rotary_dim;
+    r.amplitude = amplitude;
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rotary_dim);
+        const double turns = original_len * f / (2.0 * 3.14159265358979323846);
+        const double keep =
+            original_len == 0.0 ? 0.0 : std::min(1.0, std::max(0.0, (turns - low_turns) / (high_turns - low_turns)));
+        r.freq[i] = keep * f + (1.0 - keep) * f / factor;
+    }
+    *spec = r;
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_rope(const atlaskv_rope_spec *spec, const atlaskv_rope_io *io, void *stream)
+{
+    if (!spec || !io) return fail(ATLASKV_EINVAL, "null spec or io");
+    AKV_RET(check_dtype(io->dtype));
+    AKV_RET(check_head_dim(io->head_dim));
+    if (io->H < 1) return fail(ATLASKV_EINVAL, "H = %d < 1", io->H);
+    if (io->tokens < 0) return fail(ATLASKV_EINVAL, "tokens < 0");
+    if (io->backward != 0 && io->backward != 1) return fail(ATLASKV_EINVAL, "backward is 0 or 1");
+    akv::RopeParams p;
+    AKV_RET(rope_params(spec, io->head_dim, &p));
+    if (io->tokens == 0) return ATLASKV_OK;
+    akv::RopeIo r = {};
+    int64_t xs, ys;
+    const int64_t row = (int64_t)io->H * io->head_dim;
+    AKV_RET(check_rows("x", io->x, row, io->dtype, io->x_stride, &xs));
+    AKV_RET(check_rows("y", io->y, row, io->dtype, io->y_stride, &ys));
+    if (io->x == io->y && xs != ys) return fail(ATLASKV_EINVAL, "in place needs equal strides");
+    if (!io->positions || !aligned4(io->positions)) return fail(ATLASKV_EINVAL, "null or unaligned positions");
+    r.x = io->x;
+    r.y = io->y;
+    r.pos = io->positions;
+    r.tokens = io->tokens;
+    r.xs = xs;
+    r.ys = ys;
+    r.H = io->H;
+    r.backward = io->backward;
+    const int R = 32 / (io->head_dim / 8);
+    r.heads_per_warp = rows_per_warp(io->tokens, io->H, R, num_sms());
+    const long long warps = io->tokens * ((io->H + r.heads_per_warp - 1) / r.heads_per_warp);
+    const long long blocks = (warps + akv::kRopeThreads / 32 - 1) / (akv::kRopeThreads / 32);
+    AKV_RET(check_grid(blocks));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+#define LAUNCH(T, D) akv::rope_kernel<T, D><<<(unsigned)blocks, akv::kRopeThreads, 0, s>>>(p, r)
+    AKV_TD(io->dtype, io->head_dim, LAUNCH);
+#undef LAUNCH
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_cache_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size, size_t *bytes)
+{
+    if (!bytes) return fail(ATLASKV_EINVAL, "null bytes");
+    if (n_kv_heads < 1) return fail(ATLASKV_EINVAL, "n_kv_heads = %d < 1", n_kv_heads);
+    AKV_RET(check_head_dim(head_dim));
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+        return fail(ATLASKV_EUNSUPPORTED, "page_size %d (16, 32, 64, 128 or 256)", page_size);
+    *bytes = (size_t)n_kv_heads * (page_size / 16) * 20 * head_dim;
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_create_cache(const atlaskv_cache_desc *d, void *stream, atlaskv_cache **out)
+{
+    if (!d || !out) return fail(ATLASKV_EINVAL, "null desc or out");
+    size_t page = 0;
+    AKV_RET(atlaskv_cache_page_bytes(d->n_kv_heads, d->head_dim, d->page_size, &page));
+    if (d->n_pages < 1 || d->n_pages > 0x7fffffffLL) return fail(ATLASKV_EINVAL, "n_pages not in [1, 2^31 - 1]");
+    if (!d->pages || !aligned16(d->pages)) return fail(ATLASKV_EINVAL, "pages must be a 16-byte aligned device pointer");
+    atlaskv_cache *c = new (std::nothrow) atlaskv_cache{};
+    if (!c) return fail(ATLASKV_ENOMEM, "out of host memory");
+    c->d = *d;
+    const auto init = [&]() -> atlaskv_status {
+        AKV_CUDA(cudaGetDevice(&c->device));
+        c->num_sms = num_sms();
+        AKV_CUDA(cudaMalloc(&c->status, sizeof(int)));
+        AKV_CUDA(cudaMemsetAsync(c->status, 0, sizeof(int), static_cast<cudaStream_t>(stream)));
+        AKV_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
+        return ATLASKV_OK;
+    };
+    const atlaskv_status st = init();
+    if (st != ATLASKV_OK) {
+        if (c->status) cudaFree(c->status);
+        delete c;
+        return st;
+    }
+    *out = c;
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_destroy_cache(atlaskv_cache *c)
+{
+    if (!c) return ATLASKV_OK;
+    const cudaError_t e = cudaFree(c->status);
+    delete c;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ATLASKV_ECUDA, "cudaFree: %s", cudaGetErrorString(e));
+    }
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_cache_sync_status(atlaskv_cache *c, void *stream)
+{
+    AKV_RET(check_cache(c));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int v = 0;
+    AKV_CUDA(cudaMemcpyAsync(&v, c->status, sizeof(int), cudaMemcpyDeviceToHost, s));
+    AKV_CUDA(cudaStreamSynchronize(s));
+    if (v == akv::kDevBadPage)
+        return fail(ATLASKV_EDEVICE, "a page id, a sequence length or a slot was out of range on the device");
+    if (v == akv::kDevNonFinite) return fail(ATLASKV_EDEVICE, "a key or value to store was not finite");
+    if (v == akv::kDevTimeout) return fail(ATLASKV_ETIMEOUT, "a bounded device wait gave up");
+    if (v != akv::kDevOk) return fail(ATLASKV_EDEVICE, "device status %d", v);
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_cache_append(atlaskv_cache *c, const atlaskv_rope_spec *rope, const atlaskv_seqs *seqs,
+                                    const atlaskv_append_io *io, void *stream)
+{
+    AKV_RET(check_cache(c));
+    if (!io) return fail(ATLASKV_EINVAL, "null io");
+    AKV_RET(check_dtype(io->dtype));
+    if (io->H < 0) return fail(ATLASKV_EINVAL, "H = %d < 0", io->H);
+    akv::CacheParams p;
+    AKV_RET(cache_params(c, seqs, &p));
+    akv::RopeParams rp;
+    AKV_RET(rope_params(rope, c->d.head_dim, &rp));
+    if (seqs->B == 0) return ATLASKV_OK;
+    const int D = c->d.head_dim;
+    akv::AppendIo a = {};
+    int64_t ks, vs, qs = 0;
+    AKV_RET(check_rows("k", io->k, (int64_t)p.H_kv * D, io->dtype, io->k_stride, &ks));
+    AKV_RET(check_rows("v", io->v, (int64_t)p.H_kv * D, io->dtype, io->v_stride, &vs));
+    if (io->H > 0) {
+        AKV_RET(check_rows("q", io->q, (int64_t)io->H * D, io->dtype, io->q_stride, &qs));
+        if (!io->q_out || !aligned16(io->q_out)) return fail(ATLASKV_EINVAL, "null or unaligned q_out");
+        if (io->q_out == io->q && qs != (int64_t)io->H * D) return fail(ATLASKV_EINVAL, "in place needs a dense q");
+    }
+    if (io->positions && !aligned4(io->positions)) return fail(ATLASKV_EINVAL, "unaligned positions");
+    a.k = io->k;
+    a.v = io->v;
+    a.q = io->q;
+    a.q_out = io->q_out;
+    a.ks = ks;
+    a.vs = vs;
+    a.qs = qs;
+    a.pos = io->positions;
+    a.H = io->H;
+    const int R = 32 / (D / 8), rows = 2 * p.H_kv + io->H;
+    const long long tokens = (long long)p.B * p.N;
+    a.rows_per_warp = rows_per_warp(tokens, rows, R, c->num_sms);
+    const long long warps = tokens * ((rows + a.rows_per_warp - 1) / a.rows_per_warp);
+    const long long blocks = (warps + akv::kAppendThreads / 32 - 1) / (akv::kAppendThreads / 32);
+    AKV_RET(check_grid(blocks));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+#define LAUNCH(T, D) akv::cache_append_kernel<T, D><<<(unsigned)blocks, akv::kAppendThreads, 0, s>>>(rp, p, a)
+    AKV_TD(io->dtype, D, LAUNCH);
+#undef LAUNCH
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_cache_read(atlaskv_cache *c, const atlaskv_seqs *seqs, int32_t dtype, void *k_out, void *v_out,
+                                  void *stream)
+{
+    AKV_RET(check_cache(c));
+    AKV_RET(check_dtype(dtype));
+    akv::CacheParams p;
+    AKV_RET(cache_params(c, seqs, &p));
+    if (!aligned16(k_out) || !aligned16(v_out)) return fail(ATLASKV_EINVAL, "k_out and v_out must be 16-byte aligned");
+    if (seqs->B == 0 || (!k_out && !v_out)) return ATLASKV_OK;
+    const int D = c->d.head_dim, per_block = 8 * (32 / (D / 8));
+    const long long rows = (long long)p.B * p.N * p.H_kv, blocks = (rows + per_block - 1) / per_block;
+    AKV_RET(check_grid(blocks));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+#define LAUNCH(T, D) \
+    akv::cache_read_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(p, static_cast<T *>(k_out), static_cast<T *>(v_out))
+    AKV_TD(dtype, D, LAUNCH);
+#undef LAUNCH
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *c, int32_t dtype, int32_t B, int32_t N, int32_t H,
+                                            size_t *bytes)
+{
+    if (!c || !bytes) return fail(ATLASKV_EINVAL, "null cache or bytes");
+    AKV_RET(check_dtype(dtype));
+    if (B < 0 || N < 1 || H < 1 || H % c->d.n_kv_heads)
+        return fail(ATLASKV_EINVAL, "need B >= 0, N >= 1 and H a positive multiple of H_kv = %d", c->d.n_kv_heads);
+    *bytes = 0;
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_cache_attend(atlaskv_cache *c, const atlaskv_seqs *seqs, const atlaskv_cache_attend_io *io,
+                                    void *workspace, size_t workspace_bytes, void *stream)
+{
+    AKV_RET(check_cache(c));
+    if (!io) return fail(ATLASKV_EINVAL, "null io");
+    akv::CacheParams p;
+    AKV_RET(cache_params(c, seqs, &p));
+    size_t need = 0;
+    AKV_RET(atlaskv_cache_workspace_size(c, io->dtype, seqs->B, seqs->N, io->H, &need));
+    if (!(io->scale >= 0.f) || std::isinf(io->scale)) return fail(ATLASKV_EINVAL, "scale must be finite and >= 0");
+    if (seqs->B == 0) return ATLASKV_OK;
+    const int D = c->d.head_dim;
+    akv::CacheAttendIo a = {};
+    int64_t qs;
+    AKV_RET(check_rows("q", io->q, (int64_t)io->H * D, io->dtype, io->q_stride, &qs));
+    if (!io->out || !aligned16(io->out)) return fail(ATLASKV_EINVAL, "null or unaligned out");
+    if (io->lse && !aligned4(io->lse)) return fail(ATLASKV_EINVAL, "unaligned lse");
+    if (need > 0 && (!workspace || ((uintptr_t)workspace & 255u)))
+        return fail(ATLASKV_EINVAL, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(ATLASKV_ENOMEM, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    a.q = io->q;
+    a.out = io->out;
+    a.lse = io->lse;
+    a.qs = qs;
+    a.H = io->H;
+    a.G = io->H / p.H_kv;
+    a.scale_log2 = (io->scale > 0.f ? io->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+    const long long blocks = ((long long)p.B * p.N * io->H + 3) / 4;
+    AKV_RET(check_grid(blocks));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+#define LAUNCH(T, D) akv::cache_attend_simple_kernel<T, D><<<(unsigned)blocks, 128, 0, s>>>(p, a)
+    AKV_TD(io->dtype, D, LAUNCH);
+#undef LAUNCH
+    return ATLASKV_OK;
+}
+
+}  // extern "C"

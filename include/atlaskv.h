@@ -345,6 +345,160 @@ atlaskv_status atlaskv_attend_static(atlaskv_tree *tree, const atlaskv_params *p
  * made for the purpose.  Returns ECUDA if the launch fails. */
 atlaskv_status atlaskv_probe_wait_timeout(atlaskv_tree *tree, void *stream);
 
+/* ---- Rotary positions ------------------------------------------------------
+ * The sequence's queries and keys carry their positions as rotations: pair i of
+ * a head's first rotary_dim channels is turned by position * freq[i] radians
+ * and multiplied by the amplitude; the other channels pass through.  The pairs
+ * are channels (i, i + rotary_dim / 2) (HALF) or (2 i, 2 i + 1) (INTERLEAVED).
+ * Knowledge keys and q_kg have no position and are not rotated.  Angles are
+ * reduced in float64, so far positions lose nothing; the rotation is float32
+ * arithmetic, rounded once to the tensor's type. */
+typedef enum { ATLASKV_ROPE_HALF = 0, ATLASKV_ROPE_INTERLEAVED = 1 } atlaskv_rope_layout;
+#define ATLASKV_ROPE_MAX_PAIRS 64
+
+typedef struct {
+    int32_t layout;                          /* atlaskv_rope_layout */
+    int32_t rotary_dim;                      /* a multiple of 16, 16 <= rotary_dim <= head_dim */
+    float amplitude;                         /* finite; 1 for a plain rotation */
+    double freq[ATLASKV_ROPE_MAX_PAIRS];     /* radians per position of pair i < rotary_dim / 2 */
+} atlaskv_rope_spec;
+
+/* Fill *spec (host only).  freq[i] = base^(-2 i / rotary_dim), rescaled for
+ * contexts `factor` times as long as the original_len positions the model knew:
+ * a frequency that turns fewer than low_turns times over original_len
+ * positions is divided by factor, one that turns more than high_turns times is
+ * kept, and those between are mixed linearly in their number of turns.
+ * original_len = 0 divides every frequency by factor.  EINVAL unless base,
+ * factor > 0, original_len >= 0 and 0 <= low_turns < high_turns are finite. */
+atlaskv_status atlaskv_rope_init(atlaskv_rope_spec *spec, int32_t layout, int32_t rotary_dim, double base,
+                                 double factor, double original_len, double low_turns, double high_turns,
+                                 float amplitude);
+
+typedef struct {
+    int32_t dtype;             /* atlaskv_dtype of x and y */
+    int32_t H;                 /* heads per token, >= 1 */
+    int32_t head_dim;          /* D: 64 or 128 */
+    int64_t tokens;            /* >= 0 */
+    const void *x;             /* [tokens][H][D], token t at x + t * x_stride elements */
+    int64_t x_stride;          /* 0: dense (H * D); else >= H * D, 16 bytes divide its byte size */
+    const int32_t *positions;  /* [tokens]; any value, negative ones too */
+    void *y;                   /* like x; may be x itself (same stride), else must not overlap it */
+    int64_t y_stride;
+    int32_t backward;          /* 0: rotate.  1: the transpose, which turns a gradient of y into that of x */
+} atlaskv_rope_io;
+
+/* Rotate x into y on `stream`.  EINVAL / EUNSUPPORTED as the fields say. */
+atlaskv_status atlaskv_rope(const atlaskv_rope_spec *spec, const atlaskv_rope_io *io, void *stream);
+
+/* ---- A paged cache of the sequence's keys and values in 4 bits ---------------
+ * Slot i of a sequence (its i-th token) lives in page block_table[i /
+ * page_size], row i % page_size.  A page holds, for every KV head,
+ * page_size / 16 blocks of 16 tokens; a block is 20 D contiguous bytes:
+ *   [0, 8 D)       key codes, token t's row at t D / 2: channel 2 j in the low
+ *                  nibble of byte j, channel 2 j + 1 in its high nibble
+ *   [8 D, 10 D)    key pairs, (scale, minimum) bfloat16 per token and group of
+ *                  32 channels: [16 tokens][D / 32 groups][2]
+ *   [10 D, 18 D)   value codes, [2 halves][8 slices][4 token pairs][2 tokens]
+ *                  [D / 16 bytes]: token = 8 half + 2 pair + odd, a slice is D / 8
+ *                  channels, nibbles as for the keys
+ *   [18 D, 20 D)   value pairs, [2 halves][D / 32 groups][4 token pairs]
+ *                  [scale, minimum][2 tokens]
+ * so that one copy brings a block, and its codes lie as the matrix
+ * instructions want them.  The number stored for code c is
+ *   bfloat16(minimum + c * scale)      (one rounding, to nearest even).
+ * Storing a group of 32 float32 numbers x: minimum = the smallest x rounded
+ * down to bfloat16, scale = (largest x - minimum) / 15 rounded up to bfloat16
+ * (0 when below 2^-100), c = (x - minimum) / scale rounded to nearest even and
+ * clamped to 0 .. 15.  A stored number differs from x by at most scale / 2,
+ * plus its own rounding to bfloat16 (2^-9 of its magnitude).  Numbers above
+ * 2^120 in magnitude are stored as 2^120, NaN as 0; a non-finite number also
+ * sets EDEVICE in the cache's sticky status, so that one bad token does not
+ * reach the other sequences unnoticed.
+ *
+ * Device-side data are checked where they are used: a page id outside the
+ * pool, a length beyond the block table, more new tokens than rows, or a
+ * token below slot 0 (append, read) sets EDEVICE in the cache's status, read by
+ * atlaskv_cache_sync_status(); nothing outside the caller's buffers is
+ * touched, and that sequence's results are unspecified. */
+typedef struct {
+    int32_t n_kv_heads;        /* H_kv >= 1 */
+    int32_t head_dim;          /* D: 64 or 128 */
+    int32_t page_size;         /* tokens per page: 16, 32, 64, 128 or 256 */
+    int64_t n_pages;           /* pages in the pool, 1 .. 2^31 - 1 */
+    void *pages;               /* device, [n_pages][H_kv][page_size / 16][20 D bytes], 16-byte aligned; borrowed */
+} atlaskv_cache_desc;
+
+typedef struct atlaskv_cache atlaskv_cache;
+
+/* One batch's sequences (device arrays; read when the call runs). */
+typedef struct {
+    int32_t B;                 /* sequences, >= 0 (0: nothing to do) */
+    int32_t N;                 /* rows of the padded token tensors per sequence, >= 1 */
+    int32_t max_pages;         /* block_table columns, >= 1 */
+    const int32_t *block_table;  /* [B][max_pages] page ids; columns past a sequence's length are not read */
+    const int32_t *kv_len;     /* [B] tokens of the sequence, the new ones among them */
+    const int32_t *q_len;      /* [B] new tokens, 0 .. N, or NULL: N each.  Row n < q_len[b] of a token tensor is
+                                  slot kv_len[b] - q_len[b] + n; rows n >= q_len[b] are padding: not read, and
+                                  left as they are in outputs */
+} atlaskv_seqs;
+
+/* Bytes of one page (host only). */
+atlaskv_status atlaskv_cache_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size, size_t *bytes);
+
+/* Register a page pool on the current device.  Allocates the status word
+ * (device) and synchronises `stream`.  The pool's contents are not touched. */
+atlaskv_status atlaskv_create_cache(const atlaskv_cache_desc *desc, void *stream, atlaskv_cache **out);
+atlaskv_status atlaskv_destroy_cache(atlaskv_cache *cache);
+
+/* Synchronise `stream` and return the cache's sticky device status. */
+atlaskv_status atlaskv_cache_sync_status(atlaskv_cache *cache, void *stream);
+
+typedef struct {
+    int32_t dtype;             /* atlaskv_dtype of k, v, q and q_out */
+    const void *k, *v;         /* [B][N][H_kv][D] new tokens */
+    int64_t k_stride, v_stride;  /* elements between consecutive tokens (b * N + n); 0: dense */
+    const int32_t *positions;  /* [B][N] rotary positions, or NULL: the slots */
+    int32_t H;                 /* query heads, or 0: no queries */
+    const void *q;             /* [B][N][H][D] queries to rotate along */
+    int64_t q_stride;
+    void *q_out;               /* [B][N][H][D] dense; may be q when that is dense */
+} atlaskv_append_io;
+
+/* Rotate the new keys by their positions (rope NULL: leave them), store keys
+ * and values in their slots, and rotate the queries into q_out in the same
+ * launch.  Slots that other calls read at the same time, or that two rows of
+ * the batch share, race: the caller keeps them apart. */
+atlaskv_status atlaskv_cache_append(atlaskv_cache *cache, const atlaskv_rope_spec *rope, const atlaskv_seqs *seqs,
+                                    const atlaskv_append_io *io, void *stream);
+
+/* Read the q_len[b] newest slots of each sequence back into k_out, v_out
+ * [B][N][H_kv][D] (dense; either may be NULL) as `dtype`: the k_seq / v_seq
+ * layout of atlaskv_attend.  With q_len = kv_len that is the whole history. */
+atlaskv_status atlaskv_cache_read(atlaskv_cache *cache, const atlaskv_seqs *seqs, int32_t dtype, void *k_out,
+                                  void *v_out, void *stream);
+
+typedef struct {
+    int32_t dtype;             /* atlaskv_dtype of q and out */
+    int32_t H;                 /* query heads, a multiple of H_kv */
+    const void *q;             /* [B][N][H][D] */
+    int64_t q_stride;          /* elements between consecutive tokens; 0: dense */
+    void *out;                 /* [B][N][H][D] dense */
+    float *lse;                /* [B][N][H] natural log, optional */
+    float scale;               /* logit scale; 0 means 1/sqrt(D) */
+} atlaskv_cache_attend_io;
+
+/* Causal attention of the new tokens over their sequences' stored keys and
+ * values: row n sees slots 0 .. kv_len - q_len + n.  A row that sees nothing
+ * (kv_len < q_len, or kv_len = 0) gets out = 0 and lse = -infinity.  The new
+ * tokens themselves must have been appended before.  Workspace: device memory
+ * of atlaskv_cache_workspace_size() bytes, 256-byte aligned, not shared with
+ * a concurrent call; it depends on the sizes, not on the lengths, and need not
+ * be cleared, so a captured call may be replayed with other lengths. */
+atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *cache, int32_t dtype, int32_t B, int32_t N, int32_t H,
+                                            size_t *bytes);
+atlaskv_status atlaskv_cache_attend(atlaskv_cache *cache, const atlaskv_seqs *seqs, const atlaskv_cache_attend_io *io,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Release the handle and the small device buffers it owns; the caller's
  * buffers are untouched.  NULL is accepted. */
 atlaskv_status atlaskv_destroy(atlaskv_tree *tree);
