@@ -123,6 +123,8 @@ atlaskv_status akv_report(atlaskv_status st, const char *msg)
     return st;
 }
 
+atlaskv_status akv_smem_limit(const void *kernel, size_t bytes) { return ensure_smem(kernel, bytes); }
+
 struct atlaskv_tree {
     atlaskv_tree_desc d;
     int n_levels;                  // 3 for a uniform tree, 2 .. 4 for a CSR tree

@@ -164,6 +164,66 @@ atlaskv_status cache_params(const atlaskv_cache *c, const atlaskv_seqs *s, akv::
     return ATLASKV_OK;
 }
 
+// Row blocks of 8, 16 or 32 rows: the fewest that hold a KV head's rows (a
+// unit's codes are turned into bfloat16 once per row block).
+int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+template <typename T, int D, int NT>
+int ca_ctas(const atlaskv_cache *c)
+{
+    return akv::Ca<T, D, NT>::kCtas * c->num_sms;
+}
+
+template <typename T, int D, int NT>
+size_t ca_workspace(const atlaskv_cache *c)
+{
+    const size_t n = ca_ctas<T, D, NT>(c);
+    return n * sizeof(akv::CaDesc) + n * 2 * akv::Ca<T, D, NT>::kSlot * sizeof(float);
+}
+
+// Launch with programmatic stream serialization (the kernel begins while the
+// one before it drains, and waits before it reads or writes).
+template <typename... KArgs, typename... Args>
+atlaskv_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    AKV_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return ATLASKV_OK;
+}
+
+template <typename T, int D, int NT>
+atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, const akv::CacheAttendIo &a, cudaStream_t s)
+{
+    using C = akv::Ca<T, D, NT>;
+    AKV_RET(akv_smem_limit(reinterpret_cast<const void *>(akv::cache_attend_kernel<T, D, NT>), C::kSmem));
+    const int n = ca_ctas<T, D, NT>(c);
+    AKV_RET(launch_pdl(akv::cache_attend_kernel<T, D, NT>, dim3(n), akv::kCaThreads, C::kSmem, s, p, a));
+    return launch_pdl(akv::cache_combine_kernel<T, D, NT>, dim3(n - 1, C::kRB / 2), akv::kJoinThreads, 0, s, p, a, n);
+}
+
+// f<T, D, NT>(args...) for the call's type, head dimension and rows
+#define AKV_CA(dtype, D, NT, f, ...)                                                                              \
+    ((dtype) == ATLASKV_F32                                                                                       \
+         ? ((D) == 64 ? ((NT) == 1 ? f<float, 64, 1>(__VA_ARGS__) : (NT) == 2 ? f<float, 64, 2>(__VA_ARGS__)      \
+                                                                              : f<float, 64, 4>(__VA_ARGS__))     \
+                      : ((NT) == 1 ? f<float, 128, 1>(__VA_ARGS__) : (NT) == 2 ? f<float, 128, 2>(__VA_ARGS__)    \
+                                                                               : f<float, 128, 4>(__VA_ARGS__)))  \
+         : ((D) == 64 ? ((NT) == 1   ? f<__nv_bfloat16, 64, 1>(__VA_ARGS__)                                       \
+                         : (NT) == 2 ? f<__nv_bfloat16, 64, 2>(__VA_ARGS__)                                       \
+                                     : f<__nv_bfloat16, 64, 4>(__VA_ARGS__))                                      \
+                      : ((NT) == 1   ? f<__nv_bfloat16, 128, 1>(__VA_ARGS__)                                      \
+                         : (NT) == 2 ? f<__nv_bfloat16, 128, 2>(__VA_ARGS__)                                      \
+                                     : f<__nv_bfloat16, 128, 4>(__VA_ARGS__))))
+
 // kernel<T, D>(args...) for the call's type and head dimension
 #define AKV_TD(dtype, D, LAUNCH)                                                     \
     do {                                                                             \
@@ -387,6 +447,7 @@ atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *c, int32_t dtyp
     if (B < 0 || N < 1 || H < 1 || H % c->d.n_kv_heads)
         return fail(ATLASKV_EINVAL, "need B >= 0, N >= 1 and H a positive multiple of H_kv = %d", c->d.n_kv_heads);
     *bytes = 0;
+    if (B > 0) *bytes = AKV_CA(dtype, c->d.head_dim, row_tiles((long long)N * (H / c->d.n_kv_heads)), ca_workspace, c);
     return ATLASKV_OK;
 }
 
@@ -418,13 +479,11 @@ atlaskv_status atlaskv_cache_attend(atlaskv_cache *c, const atlaskv_seqs *seqs, 
     a.H = io->H;
     a.G = io->H / p.H_kv;
     a.scale_log2 = (io->scale > 0.f ? io->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-    const long long blocks = ((long long)p.B * p.N * io->H + 3) / 4;
-    AKV_RET(check_grid(blocks));
+    a.ws = static_cast<uint8_t *>(workspace);
+    const long long rows = (long long)p.N * a.G;
+    if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define LAUNCH(T, D) akv::cache_attend_simple_kernel<T, D><<<(unsigned)blocks, 128, 0, s>>>(p, a)
-    AKV_TD(io->dtype, D, LAUNCH);
-#undef LAUNCH
-    return ATLASKV_OK;
+    return AKV_CA(io->dtype, D, row_tiles(rows), launch_ca, c, p, a, s);
 }
 
 }  // extern "C"

@@ -2,74 +2,656 @@
 #pragma once
 
 #include "kvcache.cuh"
+#include "tcgen05.cuh"
 
 namespace akv {
 
 struct CacheAttendIo {
     const void *q;
-    void *out;          // [B][N][H][D], or null
+    void *out;          // [B][N][H][D]
     float *lse;         // [B][N][H], or null
     long long qs;       // token stride of q in elements
     int H, G;
     float scale_log2;   // scale * log2(e)
+    uint8_t *ws;        // workspace
 };
 
-// One warp per (sequence, token, query head), CUDA cores.
+// Four channels of one row's result: O / L, and the log-sum-exp with the first.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) cache_attend_simple_kernel(const CacheParams c, const CacheAttendIo io)
+__device__ __forceinline__ void ca_write(const CacheParams &c, const CacheAttendIo &io, int b, int hkv, int row, int d4,
+                                         float4 o, float M, float L)
 {
-    constexpr int PER = D / 32;
-    using B = Blk<D>;
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (long long)c.B * c.N * io.H) return;
-    const int h = (int)(row % io.H);
-    const long long tok = row / io.H;
-    const int b = (int)(tok / c.N), n = (int)(tok - (long long)b * c.N);
-    const Seq s = load_seq(c, b);
-    if (n >= s.q) return;
-    const int last = s.kv - s.q + n, hkv = h / io.G;
-    const T *q = reinterpret_cast<const T *>(io.q) + tok * io.qs + (size_t)h * D + lane * PER;
-    float qv[PER], acc[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        qv[i] = elem_f32(q[i]);
-        acc[i] = 0.f;
+    const int n = row / io.G, g = row - n * io.G;
+    const size_t at = ((size_t)b * c.N + n) * io.H + hkv * io.G + g;
+    const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;   // nothing visible: 0; NaN stays
+    T *dst = reinterpret_cast<T *>(io.out) + at * D + d4;
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), e = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&e));
     }
-    const int ch = lane * PER, g = ch / 32, r = ch / (D / 8);
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i <= last; ++i) {
-        const uint8_t *blk = block_at<D>(c, c.table[(size_t)b * c.max_pages + i / c.page_size], hkv, i);
-        if (!blk) continue;
-        const int t = i & 15;
-        const __nv_bfloat162 kp = *reinterpret_cast<const __nv_bfloat162 *>(blk + B::k_pair(t, g));
-        const __nv_bfloat16 *vp = reinterpret_cast<const __nv_bfloat16 *>(blk + B::v_scale(t, g));
-        const uint8_t *kc = blk + B::k_codes(t) + ch / 2;
-        const uint8_t *vc = blk + B::v_codes(t, r) + (ch % (D / 8)) / 2;
-        float dot = 0.f, v[PER];
+    if (io.lse && d4 == 0) io.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
+// ---- few query rows per KV head: decode and short drafts -------------------------
+//
+// For one KV head the query rows are (token n, head g of the group), row
+// n G + g; a unit of work is 32 stored tokens against a block of 8 NT rows.
+// Per row the online softmax keeps a running maximum m, sum l and output O:
+//     S = q k;  p = 2^(S scale log2 e - m);  l += sum p;  O += p v.
+// What bounds it: the codes are read once and every code becomes a bfloat16
+// (an AND-OR into the mantissa of 128, minus 128, one fused multiply-add with
+// the group's scale and minimum: exactly the stored number), about 0.8
+// instructions a code against 0.625 bytes, so HBM and the issue slots are both
+// near their limits.
+//
+// The products run on m16n8k16 with the cache as the 16-row operand, S^T = K
+// Q^T and O^T = V^T P^T: a decode step has few rows, so they take the 8-wide
+// side (tcgen05 has 128-row operands only, and its operands go through shared
+// memory or TMEM, while here a lane's codes become its own fragment in
+// registers).  The order of channels in the contraction and of output channels
+// is free, which lets a lane read its codes in 16-byte pieces.  P^T comes from
+// S^T by transposing 8 x 8 tiles between lanes (movmatrix).
+//
+// Work is split over sequences, KV heads and tokens alike: the units of all
+// (sequence, KV head, row block) items in order are cut into equal runs, one per
+// CTA, from the lengths on the device.  An item inside a run is finished there;
+// an item that a cut divides leaves partial (O, m, l) in the workspace, which
+// cache_combine_kernel joins.  Four warps of a CTA take units in turn, each
+// with a ring of bulk copies (a unit of a page is contiguous) of its own, and
+// join their rows in shared memory at the end of an item.
+
+constexpr int kCaWarps = 4;
+constexpr int kCaThreads = 32 * kCaWarps;
+constexpr int kCaUnit = 32;   // stored tokens of a unit: two blocks
+
+template <typename T, int D, int NT>
+struct Ca {
+    static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;   // bfloat16 parts of a query element and of a probability
+    static constexpr int kRB = 8 * NT;                      // rows of a row block
+    static constexpr bool kQRegs = NT * kParts <= 2;        // query fragments in registers, else in shared memory
+    static constexpr int kCtas = NT * kParts == 1 ? 4 : NT * kParts == 2 ? 3 : 2;   // per SM
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kUnitBytes = 2 * Blk<D>::kBytes;
+    static constexpr int kRing = kCaWarps * kStages * kUnitBytes;
+    static constexpr int kMergeRow = D + 4;                 // floats
+    static constexpr int kMerge = kCaWarps * 8 * (kMergeRow + 2) * 4;   // overlays the ring
+    static_assert(kMerge <= kRing, "the merge buffer overlays the ring");
+    static constexpr int kOffQ = kRing;
+    static constexpr int kQBytes = kQRegs ? 0 : kParts * NT * (D / 16) * 32 * 8;
+    static constexpr int kOffBar = kOffQ + kQBytes;
+    static constexpr int kSmem = kOffBar + kCaWarps * kStages * 8;
+    static constexpr int kSlot = kRB * (D + 2);             // floats of a partial: O, m, l
+};
+
+// What CTA c left for the join: its first item, where in it the CTA began.
+struct CaDesc {
+    long long total;        // units of the call
+    int active;             // CTAs with units
+    int k0, units;          // first unit within the item (0: not divided before it); the item's units
+    int b, hkv, rb;
+};
+
+__device__ __forceinline__ long long ca_start(long long total, int active, int c) { return total * c / active; }
+
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, const uint32_t *b)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// Two codes at bits 0..3 and 16..19 -> bf16x2 of the stored numbers.
+__device__ __forceinline__ uint32_t stored2(uint32_t x, uint32_t scale2, uint32_t low2)
+{
+    uint32_t c, r;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(c) : "r"(x));   // (x & mask) | 128.0
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c), "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(scale2), "r"(low2));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(mbar)
+                 : "memory");
+}
+
+// 8 query channels as kParts x 4 bf16 pairs (channel i, channel i + 4): the
+// float32 value is the exact sum of three bfloat16 parts.
+template <typename T>
+__device__ __forceinline__ void query_pairs(const float *x, uint32_t (*out)[4])
+{
+    float rest[8];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const int sh = 4 * (e & 1);
-            const float k = __bfloat162float(__hfma(__float2bfloat16((float)((kc[e / 2] >> sh) & 15)), kp.x, kp.y));
-            v[e] = __bfloat162float(__hfma(__float2bfloat16((float)((vc[e / 2] >> sh) & 15)), vp[0], vp[2]));
-            dot = fmaf(qv[e], k, dot);
+    for (int e = 0; e < 8; ++e) rest[e] = x[e];
+#pragma unroll
+    for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
+        float h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = __bfloat162float(__float2bfloat16(rest[e]));
+            rest[e] -= h[e];
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float x = dot * io.scale_log2, mn = fmaxf(m, x), f = exp2f(m - mn), w = exp2f(x - mn);
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[e], acc[e] * f);
-        m = mn;
+        for (int i = 0; i < 4; ++i) out[p][i] = pack_bf16(h[i], h[i + 4]);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    T *out = reinterpret_cast<T *>(io.out) + (size_t)row * D + ch;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        if constexpr (sizeof(T) == 4) out[e] = acc[e] * inv;
-        else out[e] = __float2bfloat16(acc[e] * inv);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
+    cache_attend_kernel(const CacheParams c, const CacheAttendIo io)
+{
+    using C = Ca<T, D, NT>;
+    using B = Blk<D>;
+    constexpr int P = C::kParts, KS = D / 16, S = C::kStages;
+    extern __shared__ __align__(128) uint8_t ca_smem[];
+    __shared__ long long s_sum[kCaWarps];
+    __shared__ long long s_off;
+    __shared__ int s_b;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
+    const uint32_t sb = tc::smem_addr(ca_smem);
+    const uint32_t ring = sb + warp * S * C::kUnitBytes, bars = sb + C::kOffBar + warp * S * 8;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) tc::mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (io.lse && lane == 0) io.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+    __syncwarp();
+    griddep_launch();
+    griddep_wait();
+
+    // ---- this CTA's run of units ----
+    auto n_blocks = [&](const Seq &s) { return (io.G * s.q + C::kRB - 1) / C::kRB; };
+    auto n_units = [&](const Seq &s) { return max(1, (s.kv + kCaUnit - 1) / kCaUnit); };
+    auto total_of = [&](int b) -> long long {
+        const Seq s = load_seq(c, b);
+        return (long long)c.H_kv * n_blocks(s) * n_units(s);
+    };
+    const int per = (c.B + kCaThreads - 1) / kCaThreads, b_lo = min(c.B, tid * per), b_hi = min(c.B, b_lo + per);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += total_of(b);
+    long long scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) s_sum[warp] = scan;
+    __syncthreads();
+    long long total = 0, before = scan - mine;
+#pragma unroll
+    for (int w = 0; w < kCaWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+    }
+    const int cta = blockIdx.x;
+    const int active = (int)max(1LL, min((long long)gridDim.x, (total + kCaWarps - 1) / kCaWarps));
+    CaDesc *desc = reinterpret_cast<CaDesc *>(io.ws) + cta;
+    float *slots = reinterpret_cast<float *>(io.ws + gridDim.x * sizeof(CaDesc)) + (size_t)cta * 2 * C::kSlot;
+    if (cta >= active || total == 0) {   // CTA-uniform
+        if (tid == 0) desc->k0 = 0;
+        return;
+    }
+    long long u = ca_start(total, active, cta);
+    const long long u_end = ca_start(total, active, cta + 1);
+    if (u >= before && u < before + mine) {
+        long long off = u - before;
+        int b = b_lo;
+        for (;; ++b) {
+            const long long n = total_of(b);
+            if (off < n) break;
+            off -= n;
+        }
+        s_b = b;
+        s_off = off;
+    }
+    __syncthreads();
+    int b = s_b;
+    long long off = s_off;
+
+    int T_ = 0;   // units this warp has taken from its ring
+    bool failed = false, first = true;
+    while (u < u_end) {
+        const Seq s = load_seq(c, b);
+        const int nb = n_blocks(s), units = n_units(s);
+        const long long n = (long long)c.H_kv * nb * units;
+        if (off >= n) {
+            off -= n;
+            ++b;
+            continue;
+        }
+        const int item = (int)(off / units), k0 = (int)(off - (long long)item * units);
+        const int hkv = item / nb, rb = item - hkv * nb;
+        const int cnt = (int)min((long long)(units - k0), u_end - u);
+        if (first && tid == 0) *desc = CaDesc{total, active, k0, units, b, hkv, rb};
+        const int R = io.G * s.q, row0 = rb * C::kRB;
+        // last visible slot of this lane's rows (row 2 t, 2 t + 1 of each 8), and of the block's first row
+        int lim[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                lim[j][e] = s.kv - s.q + min(row0 + 8 * j + 2 * t + e, R - 1) / io.G;
+        const int lim_first = s.kv - s.q + row0 / io.G;
+        const int lim_last = s.kv - s.q + (min(row0 + C::kRB, R) - 1) / io.G;   // and of its last row
+
+        // ---- copies ----
+        const int mine_n = cnt > warp ? (cnt - warp + kCaWarps - 1) / kCaWarps : 0;
+        const int32_t *tab = c.table + (size_t)b * c.max_pages;
+        const int pshift = 31 - __clz(c.page_size);
+        auto page_of = [&](int i, int blk) -> int {   // page of block blk of this warp's unit i
+            const int slot = (k0 + warp + kCaWarps * i) * kCaUnit + 16 * blk;
+            return i < mine_n && slot < s.kv ? tab[slot >> pshift] : 0;
+        };
+        int pg0 = page_of(lane, 0), pg1 = page_of(lane, 1), nx0 = 0, nx1 = 0;
+        if (mine_n > 32) {
+            nx0 = page_of(32 + lane, 0);
+            nx1 = page_of(32 + lane, 1);
+        }
+        auto issue = [&](int i) {   // warp-uniform i
+            const int j = i & 31;
+            if (j == 0 && i > 0) {
+                pg0 = nx0;
+                pg1 = nx1;
+                nx0 = page_of(i + 32 + lane, 0);
+                nx1 = page_of(i + 32 + lane, 1);
+            }
+            const int a = __shfl_sync(0xffffffffu, pg0, j), d = __shfl_sync(0xffffffffu, pg1, j);
+            if (lane == 0) {
+                const int key = (k0 + warp + kCaWarps * i) * kCaUnit, st = (T_ + i) % S;
+                const bool two = key + 16 < s.kv;
+                const uint32_t bar = bars + 8 * st, dst = ring + st * C::kUnitBytes;
+                const uint8_t *p0 = block_at<D>(c, a, hkv, key), *p1 = two ? block_at<D>(c, d, hkv, key + 16) : p0;
+                if (!p0) p0 = c.pages;   // reported; any page's bytes stand in
+                if (!p1) p1 = c.pages;
+                tc::mbar_arrive_expect_tx(bar, two ? 2 * B::kBytes : B::kBytes);
+                if (two && p1 == p0 + B::kBytes) {
+                    bulk_load(dst, p0, 2 * B::kBytes, bar);
+                } else {
+                    bulk_load(dst, p0, B::kBytes, bar);
+                    if (two) bulk_load(dst + B::kBytes, p1, B::kBytes, bar);
+                }
+            }
+        };
+        const int n_run = s.kv > 0 && !failed ? mine_n : 0;
+        for (int i = 0; i < min(S - 1, n_run); ++i) issue(i);
+
+        // ---- queries ----
+        uint32_t qf[C::kQRegs ? P : 1][C::kQRegs ? NT : 1][KS][2];
+        auto load_queries = [&](int j, auto &&store) {
+            const int row = row0 + 8 * j + r;
+            const bool ok = row < R;
+            const int tok = ok ? row / io.G : 0, g = ok ? row - tok * io.G : 0;
+            const T *q = reinterpret_cast<const T *>(io.q) + ((size_t)b * c.N + tok) * io.qs +
+                         (size_t)(hkv * io.G + g) * D + t * (D / 4);
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (ok) load8<T>(q + 8 * w, x);
+                uint32_t pr[P][4];
+                query_pairs<T>(x, pr);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    store(p, 2 * w, pr[p][0], pr[p][1]);
+                    store(p, 2 * w + 1, pr[p][2], pr[p][3]);
+                }
+            }
+        };
+        uint2 *q_sm = reinterpret_cast<uint2 *>(ca_smem + C::kOffQ);
+        if constexpr (C::kQRegs) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                load_queries(j, [&](int p, int ks, uint32_t x, uint32_t y) {
+                    qf[p][j][ks][0] = x;
+                    qf[p][j][ks][1] = y;
+                });
+        } else {
+            for (int j = warp; j < NT; j += kCaWarps)
+                load_queries(j, [&](int p, int ks, uint32_t x, uint32_t y) {
+                    q_sm[((p * NT + j) * KS + ks) * 32 + lane] = make_uint2(x, y);
+                });
+            __syncthreads();
+        }
+
+        float acc[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][k][e] = 0.f;
+            m[j][0] = m[j][1] = -INFINITY;
+            l[j][0] = l[j][1] = 0.f;
+        }
+
+        for (int i = 0; i < n_run; ++i) {
+            if (i + S - 1 < n_run) issue(i + S - 1);
+            const int st = (T_ + i) % S;
+            if (__any_sync(0xffffffffu, !tc::mbar_wait(bars + 8 * st, ((T_ + i) / S) & 1))) {
+                failed = true;   // the copies still in flight must land before the CTA ends
+                for (int x = i; x < min(i + S, n_run); ++x) tc::mbar_wait(bars + 8 * ((T_ + x) % S), ((T_ + x) / S) & 1);
+                break;
+            }
+            const int key0 = (k0 + warp + kCaWarps * i) * kCaUnit;
+            if (key0 > lim_last) {   // past every row of the block
+                __syncwarp();
+                continue;
+            }
+            const uint8_t *ub = ca_smem + (ring - sb) + st * C::kUnitBytes;
+            const bool two = key0 + 16 < s.kv;
+
+            float sc[2][NT][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[k][j][e] = 0.f;
+            // ---- S^T = K Q^T: a lane holds tokens r, r + 8, channels t D / 4 .. ----
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k == 1 && !two) break;
+                const uint8_t *blk = ub + k * B::kBytes;
+                uint32_t w[2][D / 32], s2[2], m2[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(blk + B::k_codes(r + 8 * h) + t * 16);
+                        w[h][0] = v.x;
+                        w[h][1] = v.y;
+                        w[h][2] = v.z;
+                        w[h][3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(blk + B::k_codes(r + 8 * h) + t * 8);
+                        w[h][0] = v.x;
+                        w[h][1] = v.y;
+                    }
+                    const uint32_t pr =
+                        *reinterpret_cast<const uint32_t *>(blk + B::k_pair(r + 8 * h, t * (D / 4) / 32));
+                    s2[h] = prmt(pr, pr, 0x1010);
+                    m2[h] = prmt(pr, pr, 0x3232);
+                }
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {   // contraction step 2 x + y
+                        uint32_t a[4];
+                        a[0] = stored2(w[0][x] >> (8 * y), s2[0], m2[0]);
+                        a[1] = stored2(w[1][x] >> (8 * y), s2[1], m2[1]);
+                        a[2] = stored2(w[0][x] >> (8 * y + 4), s2[0], m2[0]);
+                        a[3] = stored2(w[1][x] >> (8 * y + 4), s2[1], m2[1]);
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                if constexpr (C::kQRegs) {
+                                    mma16816(sc[k][j], a, qf[p][j][2 * x + y]);
+                                } else {
+                                    const uint2 v = q_sm[((p * NT + j) * KS + 2 * x + y) * 32 + lane];
+                                    const uint32_t bq[2] = {v.x, v.y};
+                                    mma16816(sc[k][j], a, bq);
+                                }
+                            }
+                    }
+            }
+
+            // ---- softmax: element (token r + 8 (e / 2), row 2 t + (e & 1)) ----
+            const bool edge = key0 + kCaUnit - 1 > min(lim_first, s.kv - 1);
+            uint32_t pf[P][NT][2][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float v[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[k][e] = sc[k][j][e] * io.scale_log2;
+                if (edge) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + 16 * k + r + 8 * (e >> 1) > lim[j][e & 1]) v[k][e] = -INFINITY;
+                }
+                float x0 = fmaxf(fmaxf(v[0][0], v[0][2]), fmaxf(v[1][0], v[1][2]));
+                float x1 = fmaxf(fmaxf(v[0][1], v[0][3]), fmaxf(v[1][1], v[1][3]));
+                // the maximum moves only when a logit exceeds it by 2^8: any m gives the same quotient O / l
+                if (__any_sync(0xffffffffu, x0 > m[j][0] + 8.f || x1 > m[j][1] + 8.f)) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+                    }
+                    const float n0 = fmaxf(m[j][0], x0), n1 = fmaxf(m[j][1], x1);
+                    const float f0 = n0 == -INFINITY ? 1.f : tc::fast_exp2(m[j][0] - n0);
+                    const float f1 = n1 == -INFINITY ? 1.f : tc::fast_exp2(m[j][1] - n1);
+                    m[j][0] = n0;
+                    m[j][1] = n1;
+                    l[j][0] *= f0;
+                    l[j][1] *= f1;
+#pragma unroll
+                    for (int d = 0; d < KS; ++d) {
+                        acc[j][d][0] *= f0;
+                        acc[j][d][2] *= f0;
+                        acc[j][d][1] *= f1;
+                        acc[j][d][3] *= f1;
+                    }
+                }
+                const float z0 = m[j][0] == -INFINITY ? 0.f : m[j][0], z1 = m[j][1] == -INFINITY ? 0.f : m[j][1];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[k][e] = tc::fast_exp2(v[k][e] - ((e & 1) ? z1 : z0));
+                    l[j][0] += v[k][0] + v[k][2];
+                    l[j][1] += v[k][1] + v[k][3];
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const uint32_t lo = pack_bf16(v[k][0], v[k][1]), hi = pack_bf16(v[k][2], v[k][3]);
+                        pf[p][j][k][0] = transpose8x8(lo);
+                        pf[p][j][k][1] = transpose8x8(hi);
+                        if (p + 1 < P) {   // what this part left
+                            v[k][0] -= __uint_as_float(lo << 16);
+                            v[k][1] -= __uint_as_float(lo & 0xffff0000u);
+                            v[k][2] -= __uint_as_float(hi << 16);
+                            v[k][3] -= __uint_as_float(hi & 0xffff0000u);
+                        }
+                    }
+                }
+            }
+
+            // ---- O^T += V^T P^T: a lane holds channels r D / 8 .., tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 ----
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k == 1 && !two) break;
+                const uint8_t *blk = ub + k * B::kBytes;
+                uint32_t x[2][D / 32], s2[2], m2[2];   // 4 channels of a token pair each
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(blk + B::kVC + h * 512 + lane * 16);
+                        x[h][0] = prmt(v.x, v.z, 0x5410);
+                        x[h][1] = prmt(v.x, v.z, 0x7632);
+                        x[h][2] = prmt(v.y, v.w, 0x5410);
+                        x[h][3] = prmt(v.y, v.w, 0x7632);
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(blk + B::kVC + h * 256 + lane * 8);
+                        x[h][0] = prmt(v.x, v.y, 0x5410);
+                        x[h][1] = prmt(v.x, v.y, 0x7632);
+                    }
+                    const uint2 pr = *reinterpret_cast<const uint2 *>(
+                        blk + B::kVS + ((h * B::kGroups + r * (D / 8) / 32) * 4 + t) * 8);
+                    s2[h] = pr.x;
+                    m2[h] = pr.y;
+                    if (edge) {   // tokens past the sequence may hold anything, NaN too
+                        const int a = key0 + 16 * k + 8 * h + 2 * t;
+                        const uint32_t keep = (a < s.kv ? 0xffffu : 0u) | (a + 1 < s.kv ? 0xffff0000u : 0u);
+                        s2[h] &= keep;
+                        m2[h] &= keep;
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {   // channels 2 d, 2 d + 1 of the slice
+                    uint32_t a[4];
+                    const int y = d >> 1, sh = 8 * (d & 1);
+                    a[0] = stored2(x[0][y] >> sh, s2[0], m2[0]);
+                    a[1] = stored2(x[0][y] >> (sh + 4), s2[0], m2[0]);
+                    a[2] = stored2(x[1][y] >> sh, s2[1], m2[1]);
+                    a[3] = stored2(x[1][y] >> (sh + 4), s2[1], m2[1]);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) mma16816(acc[j][d], a, pf[p][j][k]);
+                }
+            }
+            __syncwarp();   // the stage may be refilled
+        }
+        T_ += n_run;
+
+        // ---- join the warps' rows, 8 at a time, and write them ----
+        const bool whole = k0 == 0 && cnt == units;
+        float *slot = slots + (k0 > 0 ? 0 : C::kSlot);   // cut before: slot 0; only after: slot 1
+        float *mg = reinterpret_cast<float *>(ca_smem);
+        float *mg_m = mg + kCaWarps * 8 * C::kMergeRow, *mg_l = mg_m + kCaWarps * 8;
+        __syncthreads();   // every ring has been read
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (row0 + 8 * j >= R) break;   // CTA-uniform
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l[j][0] += __shfl_xor_sync(0xffffffffu, l[j][0], o);
+                l[j][1] += __shfl_xor_sync(0xffffffffu, l[j][1], o);
+            }
+            if (lane < 4) {
+                mg_m[warp * 8 + 2 * t] = m[j][0];
+                mg_m[warp * 8 + 2 * t + 1] = m[j][1];
+                mg_l[warp * 8 + 2 * t] = l[j][0];
+                mg_l[warp * 8 + 2 * t + 1] = l[j][1];
+            }
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+                float *o = mg + (warp * 8 + 2 * t) * C::kMergeRow + r * (D / 8) + 2 * d;
+                *reinterpret_cast<float2 *>(o) = make_float2(acc[j][d][0], acc[j][d][2]);
+                *reinterpret_cast<float2 *>(o + C::kMergeRow) = make_float2(acc[j][d][1], acc[j][d][3]);
+            }
+            __syncthreads();
+            for (int e = tid; e < 8 * D / 4; e += kCaThreads) {
+                const int rr = e / (D / 4), d4 = (e % (D / 4)) * 4, row = row0 + 8 * j + rr;
+                if (row < R) {
+                    float M = -INFINITY, L = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kCaWarps; ++w) M = fmaxf(M, mg_m[w * 8 + rr]);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < kCaWarps; ++w) {
+                        const float f = M == -INFINITY ? 0.f : tc::fast_exp2(mg_m[w * 8 + rr] - M);
+                        const float4 v = *reinterpret_cast<const float4 *>(mg + (w * 8 + rr) * C::kMergeRow + d4);
+                        L = fmaf(f, mg_l[w * 8 + rr], L);
+                        o.x = fmaf(f, v.x, o.x);
+                        o.y = fmaf(f, v.y, o.y);
+                        o.z = fmaf(f, v.z, o.z);
+                        o.w = fmaf(f, v.w, o.w);
+                    }
+                    if (whole) {
+                        ca_write<T, D>(c, io, b, hkv, row, d4, o, M, L);
+                    } else {
+                        *reinterpret_cast<float4 *>(slot + (8 * j + rr) * D + d4) = o;
+                        if (d4 == 0) {
+                            slot[C::kRB * D + 8 * j + rr] = M;
+                            slot[C::kRB * D + C::kRB + 8 * j + rr] = L;
+                        }
+                    }
+                }
+            }
+            __syncthreads();   // the buffer is reused, by the next rows or as the ring
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // plain writes above, copies next
+        __syncthreads();
+        u += cnt;
+        off += cnt;
+        first = false;
+    }
+    if (failed && lane == 0) set_status(c.status, kDevTimeout);
+}
+
+// Joins the items that the cuts between CTAs divided.  Block (c, y) looks at
+// the cut before CTA c: it acts if that is the first cut inside its item, on
+// two of the item's rows, four warps a row.  The parts lie in the CTAs' slots:
+// slot 1 of CTA c - 1, where the item began, and slot 0 of c, c + 1, ...
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const CacheParams c, const CacheAttendIo io, int ctas)
+{
+    using C = Ca<T, D, NT>;
+    constexpr int V = D / 32;   // channels per lane
+    __shared__ float part_o[8][D];
+    griddep_wait();
+    const CaDesc *desc = reinterpret_cast<const CaDesc *>(io.ws);
+    const float *slots = reinterpret_cast<const float *>(io.ws + ctas * sizeof(CaDesc));
+    const int cta = blockIdx.x + 1;
+    const CaDesc d = desc[cta];
+    if (d.k0 == 0) return;                              // no item divided here
+    const long long u = ca_start(d.total, d.active, cta), item = u - d.k0;
+    if (item < ca_start(d.total, d.active, cta - 1)) return;   // not the item's first cut
+    const int last = (int)(((item + d.units) * d.active - 1) / d.total);   // CTA of the item's last unit
+    const int parts = last - cta + 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rr = blockIdx.y * 2 + (warp >> 2), sub = warp & 3;
+    const int row = d.rb * C::kRB + rr;
+    const Seq s = load_seq(c, d.b);
+    auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * C::kSlot; };
+    const bool ok = row < io.G * s.q;
+    float M = -INFINITY, L = 0.f;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    if (ok) {   // warp-uniform
+        for (int p = lane; p < parts; p += 32) M = fmaxf(M, part(p)[C::kRB * D + rr]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float z = M == -INFINITY ? 0.f : M;
+        for (int p = lane; p < parts; p += 32)
+            L = fmaf(tc::fast_exp2(part(p)[C::kRB * D + rr] - z), part(p)[C::kRB * D + C::kRB + rr], L);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll 8
+        for (int p = sub; p < parts; p += 4) {
+            const float *q = part(p);
+            const float f = tc::fast_exp2(q[C::kRB * D + rr] - z);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(f, q[rr * D + lane * V + e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) part_o[warp][lane * V + e] = acc[e];
+    __syncthreads();
+    const int d4 = 4 * lane;
+    if (ok && sub == 0 && d4 < D) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += part_o[warp + w][d4 + e];
+        ca_write<T, D>(c, io, d.b, d.hkv, row, d4, make_float4(o[0], o[1], o[2], o[3]), M, L);
+    }
 }
 
 }  // namespace akv

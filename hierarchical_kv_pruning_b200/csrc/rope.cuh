@@ -65,13 +65,33 @@ struct RopeLane {
     bool first, active;
 };
 
+// cos and sin of `t` turns, |t| <= 1/2, times amp, each rounded once to
+// float32: the Taylor series on an eighth of a turn around the nearest quarter
+// (|x| <= pi / 4: the first terms left out are below 4e-13).  float32
+// functions lose another unit in the last place, and a key that is off by that
+// is stored under the neighbouring code more often.
 __device__ __forceinline__ void turn(int pos, double turns, float amp, float &c, float &s)
 {
     double t = (double)pos * turns;
     t -= rint(t);
-    sincospif((float)(2.0 * t), &s, &c);
-    c *= amp;
-    s *= amp;
+    const double quarter = rint(4.0 * t);
+    const double x = (t - 0.25 * quarter) * 6.283185307179586, y = x * x;
+    double a = 1.0 / 6227020800.0, e = 1.0 / 479001600.0;
+    a = fma(a, y, -1.0 / 39916800.0);
+    e = fma(e, y, -1.0 / 3628800.0);
+    a = fma(a, y, 1.0 / 362880.0);
+    e = fma(e, y, 1.0 / 40320.0);
+    a = fma(a, y, -1.0 / 5040.0);
+    e = fma(e, y, -1.0 / 720.0);
+    a = fma(a, y, 1.0 / 120.0);
+    e = fma(e, y, 1.0 / 24.0);
+    a = fma(a, y, -1.0 / 6.0);
+    e = fma(e, y, -0.5);
+    const double sn = fma(a * y, x, x) * amp, cs = fma(e, y, 1.0) * amp;
+    const int q = (int)quarter & 3;
+    const float fs = (float)sn, fc = (float)cs;
+    c = q == 0 ? fc : q == 1 ? -fs : q == 2 ? -fc : fs;
+    s = q == 0 ? fs : q == 1 ? fc : q == 2 ? -fs : -fc;
 }
 
 __device__ __forceinline__ RopeLane rope_lane(const RopeParams &p, const double *turns, int j, int pos, bool backward)
