@@ -99,7 +99,7 @@ class atlaskv_io(ctypes.Structure):
 
 
 class atlaskv_rope_spec(ctypes.Structure):
-    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("amplitude", ctypes.c_float),
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("amplitude", ctypes.c_double),
                 ("freq", ctypes.c_double * 64)]
 
 
@@ -174,8 +174,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             lib.atlaskv_probe_wait_timeout.argtypes = [V, V]
             lib.atlaskv_destroy.argtypes = [V]
             F64, SEQS = ctypes.c_double, ctypes.POINTER(atlaskv_seqs)
-            lib.atlaskv_rope_init.argtypes = [ctypes.POINTER(atlaskv_rope_spec), I32, I32, F64, F64, F64, F64, F64,
-                                              ctypes.c_float]
+            lib.atlaskv_rope_init.argtypes = [ctypes.POINTER(atlaskv_rope_spec), I32, I32, F64, F64, F64, F64, F64, F64]
             lib.atlaskv_rope.argtypes = [ctypes.POINTER(atlaskv_rope_spec), ctypes.POINTER(atlaskv_rope_io), V]
             lib.atlaskv_cache_page_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
             lib.atlaskv_create_cache.argtypes = [ctypes.POINTER(atlaskv_cache_desc), V, ctypes.POINTER(V)]

@@ -10,6 +10,7 @@
 
 #include "atlaskv.h"
 #include "cache_attend.cuh"
+#include "cache_attend_tc.cuh"
 #include "internal.h"
 #include "kvcache.cuh"
 #include "rope.cuh"
@@ -207,7 +208,34 @@ atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, cons
     AKV_RET(akv_smem_limit(reinterpret_cast<const void *>(akv::cache_attend_kernel<T, D, NT>), C::kSmem));
     const int n = ca_ctas<T, D, NT>(c);
     AKV_RET(launch_pdl(akv::cache_attend_kernel<T, D, NT>, dim3(n), akv::kCaThreads, C::kSmem, s, p, a));
-    return launch_pdl(akv::cache_combine_kernel<T, D, NT>, dim3(n - 1, C::kRB / 2), akv::kJoinThreads, 0, s, p, a, n);
+    if (n == 1) return ATLASKV_OK;   // no cuts
+    return launch_pdl(akv::cache_combine_kernel<T, D, C::kRB, 4>, dim3(n - 1, C::kRB / 2), akv::kJoinThreads, 0, s, p, a,
+                      n);
+}
+
+// Many rows of bfloat16 queries: tcgen05 (the few-rows kernel would turn the
+// codes into bfloat16 again for every 32 rows).
+bool use_tc(int dtype, long long rows) { return dtype == ATLASKV_BF16 && rows > 32; }
+
+template <int D>
+size_t tc_workspace(const atlaskv_cache *c)
+{
+    return (size_t)c->num_sms * (sizeof(akv::CaDesc) + 2 * akv::ctc::Smem<D>::kSlot * sizeof(float));
+}
+
+template <int D>
+atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, const akv::CacheAttendIo &a, cudaStream_t s)
+{
+    constexpr int RB = akv::ctc::kBlockRows;
+    const long long nb = ((long long)p.N * a.G + RB - 1) / RB;
+    if (nb * p.B * p.H_kv > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "too many query rows for one call");
+    AKV_RET(akv_smem_limit(reinterpret_cast<const void *>(akv::cache_attend_tc_kernel<D>), akv::ctc::Smem<D>::kBytes));
+    const int n = c->num_sms;
+    AKV_RET(launch_pdl(akv::cache_attend_tc_kernel<D>, dim3(n), akv::ctc::kThreads, akv::ctc::Smem<D>::kBytes, s, p, a,
+                       (int)nb));
+    if (n == 1) return ATLASKV_OK;
+    return launch_pdl(akv::cache_combine_kernel<__nv_bfloat16, D, RB, 1>, dim3(n - 1, RB / 8), akv::kJoinThreads, 0, s,
+                      p, a, n);
 }
 
 // f<T, D, NT>(args...) for the call's type, head dimension and rows
@@ -242,7 +270,7 @@ atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, cons
 extern "C" {
 
 atlaskv_status atlaskv_rope_init(atlaskv_rope_spec *spec, int32_t layout, int32_t rotary_dim, double base, double factor,
-                                 double original_len, double low_turns, double high_turns, float amplitude)
+                                 double original_len, double low_turns, double high_turns, double amplitude)
 {
     if (!spec) return fail(ATLASKV_EINVAL, "null spec");
     if (layout != ATLASKV_ROPE_HALF && layout != ATLASKV_ROPE_INTERLEAVED)
@@ -447,7 +475,10 @@ atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *c, int32_t dtyp
     if (B < 0 || N < 1 || H < 1 || H % c->d.n_kv_heads)
         return fail(ATLASKV_EINVAL, "need B >= 0, N >= 1 and H a positive multiple of H_kv = %d", c->d.n_kv_heads);
     *bytes = 0;
-    if (B > 0) *bytes = AKV_CA(dtype, c->d.head_dim, row_tiles((long long)N * (H / c->d.n_kv_heads)), ca_workspace, c);
+    if (B == 0) return ATLASKV_OK;
+    const long long rows = (long long)N * (H / c->d.n_kv_heads);
+    if (use_tc(dtype, rows)) *bytes = c->d.head_dim == 64 ? tc_workspace<64>(c) : tc_workspace<128>(c);
+    else *bytes = AKV_CA(dtype, c->d.head_dim, row_tiles(rows), ca_workspace, c);
     return ATLASKV_OK;
 }
 
@@ -483,6 +514,7 @@ atlaskv_status atlaskv_cache_attend(atlaskv_cache *c, const atlaskv_seqs *seqs, 
     const long long rows = (long long)p.N * a.G;
     if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (use_tc(io->dtype, rows)) return D == 64 ? launch_tc<64>(c, p, a, s) : launch_tc<128>(c, p, a, s);
     return AKV_CA(io->dtype, D, row_tiles(rows), launch_ca, c, p, a, s);
 }
 

@@ -593,15 +593,16 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
 
 // Joins the items that the cuts between CTAs divided.  Block (c, y) looks at
 // the cut before CTA c: it acts if that is the first cut inside its item, on
-// two of the item's rows, four warps a row.  The parts lie in the CTAs' slots:
+// 8 / W of the item's RB rows, W warps a row.  The parts lie in the CTAs' slots:
 // slot 1 of CTA c - 1, where the item began, and slot 0 of c, c + 1, ...
+// Few rows have many parts (a long cache over the whole device): W = 4.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int D, int NT>
+template <typename T, int D, int RB, int W>
 __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const CacheParams c, const CacheAttendIo io, int ctas)
 {
-    using C = Ca<T, D, NT>;
     constexpr int V = D / 32;   // channels per lane
+    constexpr int kSlot = RB * (D + 2);
     __shared__ float part_o[8][D];
     griddep_wait();
     const CaDesc *desc = reinterpret_cast<const CaDesc *>(io.ws);
@@ -614,28 +615,28 @@ __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const Cache
     const int last = (int)(((item + d.units) * d.active - 1) / d.total);   // CTA of the item's last unit
     const int parts = last - cta + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rr = blockIdx.y * 2 + (warp >> 2), sub = warp & 3;
-    const int row = d.rb * C::kRB + rr;
+    const int rr = blockIdx.y * (8 / W) + warp / W, sub = warp % W;
+    const int row = d.rb * RB + rr;
     const Seq s = load_seq(c, d.b);
-    auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * C::kSlot; };
+    auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * kSlot; };
     const bool ok = row < io.G * s.q;
     float M = -INFINITY, L = 0.f;
     float acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
     if (ok) {   // warp-uniform
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, part(p)[C::kRB * D + rr]);
+        for (int p = lane; p < parts; p += 32) M = fmaxf(M, part(p)[RB * D + rr]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         const float z = M == -INFINITY ? 0.f : M;
         for (int p = lane; p < parts; p += 32)
-            L = fmaf(tc::fast_exp2(part(p)[C::kRB * D + rr] - z), part(p)[C::kRB * D + C::kRB + rr], L);
+            L = fmaf(tc::fast_exp2(part(p)[RB * D + rr] - z), part(p)[RB * D + RB + rr], L);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
 #pragma unroll 8
-        for (int p = sub; p < parts; p += 4) {
+        for (int p = sub; p < parts; p += W) {
             const float *q = part(p);
-            const float f = tc::fast_exp2(q[C::kRB * D + rr] - z);
+            const float f = tc::fast_exp2(q[RB * D + rr] - z);
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] = fmaf(f, q[rr * D + lane * V + e], acc[e]);
         }
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const Cache
     if (ok && sub == 0 && d4 < D) {
         float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < W; ++w)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] += part_o[warp + w][d4 + e];
         ca_write<T, D>(c, io, d.b, d.hkv, row, d4, make_float4(o[0], o[1], o[2], o[3]), M, L);

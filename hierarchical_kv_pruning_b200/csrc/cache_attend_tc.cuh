@@ -1,0 +1,655 @@
+// Attention over the 4-bit cache for many query rows (prompts, query blocks):
+// bfloat16 queries on tcgen05.
+//
+// An item is a block of 256 query rows of one KV head (row n G + g: token n,
+// head g of the group), as two tiles of 128; its units are the 128-token key
+// tiles up to the last row's causal limit.  One persistent CTA per SM, 16
+// warps:
+//   copy warp       the codes of 64 tokens at a time into a three-stage ring
+//                   (bulk copies; a page's blocks of one KV head are contiguous);
+//   4 warps         turn them into bfloat16 K and V tiles in the 128-byte
+//                   swizzled operand layout (two stages each); tokens past the
+//                   sequence become zeros.  Within 8 channels a pair of a
+//                   register is (channel i, i + 4), as the nibbles come out; Q
+//                   is stored in the same order, O is put back in the epilogue;
+//   MMA thread      for each key tile, per row tile: S = Q K^T (M 128, N 128),
+//                   later O += P V with P read from TMEM, where it overlays S.
+//                   P V and the next S of one row tile run under the softmax
+//                   of the other;
+//   2 x 4 warps     softmax, one thread per row: as in the few-rows kernel.
+// TMEM: S / P 2 x 128 and O 2 x D columns.  Shared memory (D = 128): Q 64, K 64,
+// V 64, codes 30 KB.
+// What bounds it: per key tile the tensor cores need 2048 cycles (D = 128), the
+// exponentials 2048 on the MUFU pipe, operand reads and the tile writes about
+// 2400 of shared memory's.  256 rows per tile and N = 128 were chosen for the
+// last: with N = 64 the A operand is read twice as often, and with 128 rows
+// the conversion of the codes would not be shared.
+//
+// The runs of units per CTA are as in the few-rows kernel, unless whole items
+// balance about as well (a partial of 256 rows costs as much as several tiles).
+//
+// Every wait is bounded; one that gives up sets ETIMEOUT in the status word.
+#pragma once
+
+#include "cache_attend.cuh"
+
+namespace akv {
+namespace ctc {
+
+using namespace tc;
+
+constexpr int kRows = 128, kBlockRows = 256, kKeys = 128, kHalf = 64;
+constexpr int kKV = 2, kRaw = 3;    // stages of the K and V tiles, of the codes
+constexpr int kThreads = 512;
+constexpr int kDequantWarp = 8, kMmaWarp = 12, kCopyWarp = 13;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;   // 2 x 128 x (192 + 64) = the 512 x 128 of the launch
+constexpr float kRescale = 8.f;     // rescale O when a row's maximum grows by more than 2^8
+// A partial costs about this many units to write, read and join.
+constexpr int kPartialUnits = 6;
+
+constexpr int kBarRawFull = 0, kBarRawEmpty = kBarRawFull + kRaw, kBarKFull = kBarRawEmpty + kRaw,
+              kBarKEmpty = kBarKFull + kKV, kBarVFull = kBarKEmpty + kKV, kBarVEmpty = kBarVFull + kKV,
+              kBarS = kBarVEmpty + kKV, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarQ = kBarO + 2,
+              kBarDrained = kBarQ + 2, kBarEnd = kBarDrained + 2, kNumBars = kBarEnd + 1;
+
+template <int D>
+struct Smem {
+    static constexpr int kQ = kRows * D * 2, kT = kKeys * D * 2, kR = 4 * Blk<D>::kBytes;
+    static constexpr int kOffQ = 0, kOffK = 2 * kQ, kOffV = kOffK + kKV * kT, kOffR = kOffV + kKV * kT,
+                         kOffBar = kOffR + kRaw * kR, kOffSlot = kOffBar + kNumBars * 8, kOffSched = kOffSlot + 16, kBytes = kOffSched + 64;
+    static constexpr int kColS = 0, kColO = 2 * kKeys;
+    static constexpr int kSlot = kBlockRows * (D + 2);   // floats of a partial: O, m, l
+};
+
+template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// An entry: 256-row block rb of sequence b (for every KV head).
+struct Entry {
+    Seq s;
+    int b, rb, rows, units;   // rows of the block; key tiles (0: no rows)
+};
+
+// A stretch of units of one item that a CTA runs.
+struct Seg {
+    Entry e;
+    int hkv, k0, cnt;
+};
+
+// The CTA's share of the call, in shared memory.
+struct Sched {
+    long long total, off0, u0, u1;   // units of the call; start within entry e0; the CTA's units
+    int whole_items, active, e0, nb; // whole items round-robin?; CTAs with units; first entry; row blocks per sequence
+};
+
+__device__ __forceinline__ Entry entry_at(const CacheParams &c, const CacheAttendIo &io, int nb, int e)
+{
+    Entry x;
+    x.b = e / nb;
+    x.rb = e - x.b * nb;
+    x.s = load_seq(c, x.b);
+    const int R = io.G * x.s.q, row0 = x.rb * kBlockRows;
+    x.rows = max(0, min(kBlockRows, R - row0));
+    const int last = x.s.kv - x.s.q + (row0 + x.rows - 1) / io.G;
+    x.units = x.rows > 0 ? max(1, (last + kKeys) / kKeys) : 0;
+    return x;
+}
+
+// Walks the CTA's stretches; every role walks its own copy.
+struct Walk {
+    int e, item;
+    long long off, u;
+    __device__ __forceinline__ void begin(const Sched &s)
+    {
+        e = s.e0;
+        off = s.off0;
+        u = s.u0;
+        item = blockIdx.x;
+    }
+    __device__ __forceinline__ bool next(const CacheParams &c, const CacheAttendIo &io, const Sched &s, Seg &g)
+    {
+        const int nb = s.nb, entries = c.B * nb;
+        if (s.whole_items) {   // items round-robin, the long ones (late row blocks) first
+            for (; item < entries * c.H_kv; item += gridDim.x) {
+                const int x = item / c.H_kv;
+                g.e = entry_at(c, io, nb, entries - 1 - x);
+                if (g.e.units == 0) continue;
+                g.hkv = item - x * c.H_kv;
+                g.k0 = 0;
+                g.cnt = g.e.units;
+                item += gridDim.x;
+                return true;
+            }
+            return false;
+        }
+        while (u < s.u1) {
+            g.e = entry_at(c, io, nb, e);
+            const long long n = (long long)c.H_kv * g.e.units;
+            if (off >= n) {
+                off -= n;
+                ++e;
+                continue;
+            }
+            g.hkv = (int)(off / g.e.units);
+            g.k0 = (int)(off - (long long)g.hkv * g.e.units);
+            g.cnt = (int)min((long long)(g.e.units - g.k0), s.u1 - u);
+            u += g.cnt;
+            off += g.cnt;
+            return true;
+        }
+        return false;
+    }
+};
+
+}  // namespace ctc
+
+template <int D>
+__global__ void __launch_bounds__(ctc::kThreads, 1)
+    cache_attend_tc_kernel(const CacheParams c, const CacheAttendIo io, int nb)
+{
+    using namespace ctc;
+    using SM = Smem<D>;
+    using B = Blk<D>;
+    constexpr int kBlocks = D / 64;   // 64-channel column blocks of a tile
+    extern __shared__ __align__(1024) uint8_t ctc_smem[];
+    const uint32_t sb = smem_addr(ctc_smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) -> uint32_t { return sb + SM::kOffBar + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctc_smem + SM::kOffSlot);
+    // scratch of the share's scan, in the ring before its first copy (static
+    // shared memory would move the dynamic base off its 1024-byte alignment)
+    long long *s_sum = reinterpret_cast<long long *>(ctc_smem + SM::kOffR);
+    int *s_max = reinterpret_cast<int *>(s_sum + 16), *s_items = s_max + 16;
+    griddep_launch();
+    griddep_wait();
+    CaDesc *desc = reinterpret_cast<CaDesc *>(io.ws) + blockIdx.x;
+    if (tid == 0) desc->k0 = 0;   // until a stretch begins inside an item
+    if (sb & 1023u) {             // the swizzle atoms need a 1024-byte aligned base (CTA-uniform exit)
+        if (tid == 0) set_status(c.status, kDevBadSmem);
+        return;
+    }
+
+    // ---- the CTA's share ----
+    Sched &sch = *reinterpret_cast<Sched *>(ctc_smem + SM::kOffSched);
+    const int entries = c.B * nb, per = (entries + kThreads - 1) / kThreads;
+    {
+        const int lo = min(entries, tid * per), hi = min(entries, lo + per);
+        long long mine = 0;
+        int big = 0, items = 0;
+        for (int e = lo; e < hi; ++e) {
+            const int n = entry_at(c, io, nb, e).units;
+            mine += (long long)c.H_kv * n;
+            big = max(big, n);
+            items += n > 0 ? c.H_kv : 0;
+        }
+        long long scan = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+            items += __shfl_xor_sync(0xffffffffu, items, o);
+        }
+        if (lane == 31) {
+            s_sum[warp] = scan;
+            s_max[warp] = big;
+            s_items[warp] = items;
+        }
+        __syncthreads();
+        long long total = 0, before = scan - mine, all_items = 0;
+        int top = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_sum[w];
+            total += s_sum[w];
+            top = max(top, s_max[w]);
+            all_items += s_items[w];
+        }
+        const long long ctas = gridDim.x;
+        const bool whole = (all_items + ctas - 1) / ctas * top <= (total + ctas - 1) / ctas + kPartialUnits;
+        const int active = (int)max(1LL, min(ctas, total));
+        if (!whole && (total == 0 || blockIdx.x >= active)) return;   // CTA-uniform
+        if (tid == 0) {
+            sch.total = total;
+            sch.active = active;
+            sch.whole_items = whole;
+            sch.nb = nb;
+        }
+        if (!whole) {
+            const long long u0 = ca_start(total, active, blockIdx.x);
+            if (u0 >= before && u0 < before + mine) {   // one thread
+                long long off = u0 - before;
+                int e = lo;
+                for (;; ++e) {
+                    const long long n = (long long)c.H_kv * entry_at(c, io, nb, e).units;
+                    if (off < n) break;
+                    off -= n;
+                }
+                sch.e0 = e;
+                sch.off0 = off;
+                sch.u0 = u0;
+                sch.u1 = ca_start(total, active, blockIdx.x + 1);
+            }
+        }
+    }
+    if (tid == 0) {
+        fence_async_smem();   // the scratch was plainly written, copies come next
+        for (int i = 0; i < kNumBars; ++i) {
+            const bool by4 = (i >= kBarRawEmpty && i < kBarKEmpty) || (i >= kBarVFull && i < kBarVEmpty) ||
+                             (i >= kBarP && i < kBarO) || (i >= kBarQ && i < kBarEnd);
+            mbar_init(bar(i), by4 ? 4 : 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    Walk walk;
+    walk.begin(sch);
+    Seg g;
+
+    if (warp < 8) {
+        // ================= softmax: one thread per query row =================
+        regs_up<kSoftmaxRegs>();
+        const int grp = warp >> 2, lrow = tid & 127, w4 = warp & 3;
+        const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
+        const uint32_t tS = tmem + SM::kColS + grp * kKeys + lane_off, tO = tmem + SM::kColO + grp * D + lane_off;
+        uint8_t *q_tile = ctc_smem + SM::kOffQ + grp * SM::kQ;
+        bool failed = false;
+        auto next_own = [&](Seg &x) -> bool {
+            while (walk.next(c, io, sch, x))
+                if (x.e.rows > grp * kRows) return true;
+            return false;
+        };
+        // this group's 128 rows of a stretch into the swizzled A tile, zeros past its rows
+        auto load_q = [&](const Seg &x) {
+            constexpr int CPR = D / 8, RPI = 128 / CPR;   // chunks of a row; rows per step of the 128 threads
+            const int cc = lrow % CPR;
+            const int row0 = x.e.rb * kBlockRows + grp * kRows, rows = x.e.rows - grp * kRows;
+#pragma unroll 8
+            for (int i = 0; i < kRows / RPI; ++i) {
+                const int rl = i * RPI + lrow / CPR;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (rl < rows) {
+                    const int row = row0 + rl, n = row / io.G, h = row - n * io.G;
+                    v = ldg16(reinterpret_cast<const __nv_bfloat16 *>(io.q) + ((size_t)x.e.b * c.N + n) * io.qs +
+                              (size_t)(x.hkv * io.G + h) * D + cc * 8);
+                }
+                *reinterpret_cast<uint4 *>(q_tile + (cc >> 3) * (kRows * 128) + sw128(rl, cc & 7)) =
+                    make_uint4(prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632), prmt(v.y, v.w, 0x5410),
+                               prmt(v.y, v.w, 0x7632));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarQ + grp));
+        };
+        int T = 0, seg = 0;   // this group's tiles and stretches so far
+        bool more = next_own(g);
+        if (more) load_q(g);
+        bool first_seg = true;
+        while (more && !failed) {
+            const Seg cur = g;
+            const int row = cur.e.rb * kBlockRows + grp * kRows + lrow;
+            const bool row_ok = grp * kRows + lrow < cur.e.rows;
+            const int lim = row_ok ? cur.e.s.kv - cur.e.s.q + row / io.G : -1;   // last visible slot
+            // the tiles up to here need no mask
+            const int lim_first = cur.e.s.kv - cur.e.s.q + (cur.e.rb * kBlockRows + grp * kRows) / io.G;
+            const bool all_rows = cur.e.rows >= (grp + 1) * kRows;
+            float m = -INFINITY, l = 0.f;
+            for (int t = 0; t < cur.cnt; ++t, ++T) {
+                failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarS + grp), T & 1));
+                if (failed) break;
+                fence_after_sync();
+                // Two halves of 64 keys: the second is read for its maximum here and again for its
+                // probabilities below (128 logits would not fit the registers).
+                const int key0 = (cur.k0 + t) * kKeys;
+                const bool edge = !all_rows || key0 + kKeys - 1 > lim_first;   // warp-uniform
+                const int hi = lim - key0;
+                float sc[kHalf];
+                auto load_s = [&](int from) {
+                    tmem_ld32(tS + from, sc);
+                    tmem_ld32(tS + from + 32, sc + 32);
+                    tmem_wait_ld();
+                    if (edge) {
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j) sc[j] = from + j <= hi ? sc[j] : -INFINITY;
+                    }
+                };
+                float mx[8];
+                load_s(kHalf);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mx[j] = sc[j];
+#pragma unroll
+                for (int j = 8; j < kHalf; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
+                load_s(0);
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
+                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                const float m_new = fmaxf(m, top * io.scale_log2);
+                if (t == 0) {
+                    m = m_new;
+                } else {
+                    const bool need = m_new > m + kRescale;
+                    if (__any_sync(0xffffffffu, need)) {   // the previous P V landed before this S
+                        const float f = need ? fast_exp2(m - m_new) : 1.f;
+#pragma unroll
+                        for (int d = 0; d < D; d += 32) {
+                            float o[32];
+                            tmem_ld32(tO + d, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= f;
+                            tmem_st32(tO + d, o);
+                        }
+                        tmem_wait_st();
+                        if (need) {
+                            l *= f;
+                            m = m_new;
+                        }
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.f : -m;
+                float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 1) load_s(kHalf);   // P so far lies over keys 0 .. 31 of S
+#pragma unroll
+                    for (int k = 0; k < kHalf; k += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float e0 = fast_exp2(fmaf(sc[k + j], io.scale_log2, neg));
+                            const float e1 = fast_exp2(fmaf(sc[k + j + 1], io.scale_log2, neg));
+                            ps[(j >> 1) & 7] += e0 + e1;
+                            pk[j / 2] = pack_bf16(e0, e1);
+                        }
+                        tmem_st16(tS + (half * kHalf + k) / 2, pk);
+                    }
+                }
+                l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarP + grp));
+            }
+            if (failed) break;
+            // the stretch's last S is done: Q is free
+            more = next_own(g);
+            if (more) load_q(g);
+            failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarO + grp), seg & 1));   // the last P V landed
+            if (failed) break;
+            fence_after_sync();
+            // ---- out: O / l with its log-sum-exp, or a partial ----
+            const bool whole = cur.k0 == 0 && cur.cnt == cur.e.units;
+            const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+            const int n = row / io.G, h = row - n * io.G;
+            const size_t at = ((size_t)cur.e.b * c.N + n) * io.H + cur.hkv * io.G + h;
+            float *slot = reinterpret_cast<float *>(io.ws + gridDim.x * sizeof(CaDesc)) +
+                          ((size_t)blockIdx.x * 2 + (cur.k0 > 0 ? 0 : 1)) * SM::kSlot;
+            const int sr = grp * kRows + lrow;
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+                float o[32];
+                tmem_ld32(tO + d, o);
+                tmem_wait_ld();
+                if (d == D - 32) {   // O has been read: the next stretch may start it afresh
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarDrained + grp));
+                }
+                if (!row_ok) continue;
+                // position p of 8 holds channel (p >> 1) + 4 (p & 1)
+                if (whole) {
+                    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(io.out) + at * D + d;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4 *>(dst + i) =
+                            make_uint4(pack_bf16(o[i] * inv, o[i + 2] * inv), pack_bf16(o[i + 4] * inv, o[i + 6] * inv),
+                                       pack_bf16(o[i + 1] * inv, o[i + 3] * inv), pack_bf16(o[i + 5] * inv, o[i + 7] * inv));
+                } else {
+                    float *dst = slot + sr * D + d;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        *reinterpret_cast<float4 *>(dst + i) = make_float4(o[i], o[i + 2], o[i + 4], o[i + 6]);
+                        *reinterpret_cast<float4 *>(dst + i + 4) = make_float4(o[i + 1], o[i + 3], o[i + 5], o[i + 7]);
+                    }
+                }
+            }
+            if (row_ok) {
+                if (whole) {
+                    if (io.lse) io.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+                } else {
+                    slot[kBlockRows * D + sr] = m;
+                    slot[kBlockRows * D + kBlockRows + sr] = l;
+                }
+            }
+            // the join needs to know where the CTA's first stretch began (group 0 has rows in every stretch)
+            if (grp == 0 && lrow == 0 && first_seg)
+                *desc = CaDesc{sch.total, sch.active, cur.k0, cur.e.units, cur.e.b, cur.hkv, cur.e.rb};
+            first_seg = false;
+            ++seg;
+        }
+        if (failed && lane == 0) set_status(c.status, kDevTimeout);
+    } else if (warp < kMmaWarp) {
+        // ================= codes to bfloat16 tiles =================
+        regs_down<kOtherRegs>();
+        const int t128 = tid - kDequantWarp * 32, key = t128 & 63, col = t128 >> 6;   // token of the half tile; 64-channel half of a row
+            bool failed = false;
+        int T = 0;
+        while (!failed && walk.next(c, io, sch, g)) {
+            for (int t = 0; t < g.cnt; ++t, ++T) {
+                const int st = T % kKV;
+                const int key0 = (g.k0 + t) * kKeys;
+                if (T >= kKV) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarKEmpty + st), ((T / kKV) + 1) & 1));
+                if (failed) break;
+                // keys of both halves, then values
+#pragma unroll 1
+                for (int step = 0; step < 4; ++step) {
+                    const int h = step & 1, raw = 2 * T + h, rs = raw % kRaw;
+                    const bool is_v = step >= 2;
+                    if (!is_v) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarRawFull + rs), (raw / kRaw) & 1));
+                    else if (h == 0 && T >= kKV)
+                        failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarVEmpty + st), ((T / kKV) + 1) & 1));
+                    if (failed) break;
+                    const uint8_t *blk = ctc_smem + SM::kOffR + rs * SM::kR + (key >> 4) * B::kBytes;
+                    const int tok = key & 15, r = h * kHalf + key;
+                    const bool ok = key0 + r < g.e.s.kv;
+                    uint8_t *tile = ctc_smem + (is_v ? SM::kOffV : SM::kOffK) + st * SM::kT;
+                    // this thread's D / 2 channels: D / 64 groups of 32
+#pragma unroll
+                    for (int gi = 0; gi < kBlocks; ++gi) {
+                        const int gr = col * kBlocks + gi;   // group of the row
+                        uint32_t w[4], s2, m2;
+                        if (is_v) {
+                            const uint8_t *p = blk + B::v_scale(tok, gr);
+                            s2 = *reinterpret_cast<const uint16_t *>(p);
+                            m2 = *reinterpret_cast<const uint16_t *>(p + 4);
+                            s2 |= s2 << 16;
+                            m2 |= m2 << 16;
+                            if constexpr (D == 128) {
+                                const uint2 a = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr));
+                                const uint2 e = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr + 1));
+                                w[0] = a.x;
+                                w[1] = a.y;
+                                w[2] = e.x;
+                                w[3] = e.y;
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    w[i] = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(tok, 4 * gr + i));
+                            }
+                        } else {
+                            const uint32_t pr = *reinterpret_cast<const uint32_t *>(blk + B::k_pair(tok, gr));
+                            s2 = prmt(pr, pr, 0x1010);
+                            m2 = prmt(pr, pr, 0x3232);
+                            const uint4 a = *reinterpret_cast<const uint4 *>(blk + B::k_codes(tok) + gr * 16);
+                            w[0] = a.x;
+                            w[1] = a.y;
+                            w[2] = a.z;
+                            w[3] = a.w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = gr * 4 + i;   // 8-channel chunk of the row
+                            uint4 v;
+                            v.x = stored2(w[i], s2, m2);
+                            v.y = stored2(w[i] >> 4, s2, m2);
+                            v.z = stored2(w[i] >> 8, s2, m2);
+                            v.w = stored2(w[i] >> 12, s2, m2);
+                            if (!ok) v = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4 *>(tile + (ch >> 3) * (kKeys * 128) + sw128(r, ch & 7)) = v;
+                        }
+                    }
+                    if (is_v) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kBarRawEmpty + rs));
+                    }
+                    if (h == 1) {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
+                    }
+                }
+                if (failed) break;
+            }
+        }
+        if (failed && lane == 0) set_status(c.status, kDevTimeout);
+    } else {
+        regs_down<kOtherRegs>();
+        if (warp == kCopyWarp) {
+            // ================= copies of the codes, 64 tokens each =================
+            bool failed = false;
+            int raw = 0;
+            const int pshift = 31 - __clz(c.page_size);
+            while (!failed && walk.next(c, io, sch, g)) {
+                const int32_t *tab = c.table + (size_t)g.e.b * c.max_pages;
+                for (int i = 0; i < 2 * g.cnt; ++i, ++raw) {
+                    const int rs = raw % kRaw, key = g.k0 * kKeys + i * kHalf;
+                    const int blocks = max(0, min(4, (g.e.s.kv - key + 15) >> 4));
+                    // lane j: the block of tokens key + 16 j
+                    const uint8_t *src = nullptr;
+                    if (lane < blocks) {
+                        src = block_at<D>(c, tab[(key + 16 * lane) >> pshift], g.hkv, key + 16 * lane);
+                        if (!src) src = c.pages;   // reported; any page's bytes stand in
+                    }
+                    if (raw >= kRaw)
+                        failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarRawEmpty + rs), ((raw / kRaw) + 1) & 1));
+                    if (failed) break;
+                    if (lane == 0) {
+                        if (blocks > 0) mbar_arrive_expect_tx(bar(kBarRawFull + rs), blocks * B::kBytes);
+                        else mbar_arrive(bar(kBarRawFull + rs));
+                    }
+                    __syncwarp();
+                    const uint32_t dst = sb + SM::kOffR + rs * SM::kR;
+                    if (c.page_size >= kHalf) {   // 64 tokens of a page are contiguous
+                        if (lane == 0 && blocks > 0) bulk_load(dst, src, blocks * B::kBytes, bar(kBarRawFull + rs));
+                    } else if (lane < blocks) {
+                        bulk_load(dst + lane * B::kBytes, src, B::kBytes, bar(kBarRawFull + rs));
+                    }
+                }
+            }
+            // the CTA must not end with copies in flight
+            bool landed = true;
+            for (int x = max(0, raw - kRaw); x < raw; ++x) landed &= mbar_wait(bar(kBarRawFull + x % kRaw), (x / kRaw) & 1);
+            if ((failed || !landed) && lane == 0) set_status(c.status, kDevTimeout);
+        } else if (warp == kMmaWarp && lane == 0) {
+            // ================= MMA issue: one thread =================
+            const uint32_t idesc_s = make_idesc(kRows, kKeys, 0, 0), idesc_o = make_idesc(kRows, D, 0, 1);
+            const uint64_t dq0 = make_desc(sb + SM::kOffQ, 16, 1024), dk0 = make_desc(sb + SM::kOffK, 16, 1024),
+                           dv0 = make_desc(sb + SM::kOffV, kKeys * 128, 1024);
+            struct Tile {
+                int T, t, cnt;      // running count; index in its stretch and the stretch's tiles
+                bool two;           // both row tiles have rows
+            };
+            int Tg[2] = {0, 0}, Sg[2] = {0, 0};   // tiles (P phases) and stretches (Q loads) of each group so far
+            bool ok = true;
+            auto issue_s = [&](const Tile &x, int grp) -> bool {
+                if (grp == 0 && !mbar_wait(bar(kBarKFull + x.T % kKV), (x.T / kKV) & 1)) return false;
+                if (x.t == 0) {
+                    if (!mbar_wait(bar(kBarQ + grp), Sg[grp] & 1)) return false;
+                    ++Sg[grp];
+                }
+                fence_after_sync();
+                const uint64_t q = dq0 + (uint64_t)((grp * SM::kQ) >> 4), k = dk0 + (uint64_t)(((x.T % kKV) * SM::kT) >> 4);
+                const uint32_t td = tmem + SM::kColS + grp * kKeys;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(td, q + (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4),
+                             k + (uint64_t)(((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+                mma_commit(bar(kBarS + grp));
+                if (grp == 1 || !x.two) mma_commit(bar(kBarKEmpty + x.T % kKV));
+                return true;
+            };
+            auto issue_pv = [&](const Tile &x, int grp) -> bool {
+                if (grp == 0 && !mbar_wait(bar(kBarVFull + x.T % kKV), (x.T / kKV) & 1)) return false;
+                if (!mbar_wait(bar(kBarP + grp), Tg[grp] & 1)) return false;
+                ++Tg[grp];
+                // a stretch's first P V starts O afresh once the previous O has been read out
+                const int sn = Sg[grp] - 1;
+                if (x.t == 0 && sn > 0 && !mbar_wait(bar(kBarDrained + grp), (sn - 1) & 1)) return false;
+                fence_after_sync();
+                const uint64_t v = dv0 + (uint64_t)(((x.T % kKV) * SM::kT) >> 4);
+                const uint32_t ta = tmem + SM::kColS + grp * kKeys, td = tmem + SM::kColO + grp * D;
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    mma_bf16_ts(td, ta + 8 * ks, v + (uint64_t)((ks * 16 * 128) >> 4), idesc_o,
+                                (x.t > 0 || ks > 0) ? 1u : 0u);
+                if (x.t == x.cnt - 1) mma_commit(bar(kBarO + grp));
+                if (grp == 1 || !x.two) mma_commit(bar(kBarVEmpty + x.T % kKV));
+                return true;
+            };
+            Tile cur{0, 0, 0, false};
+            bool have = walk.next(c, io, sch, g);
+            if (have) {
+                cur = Tile{0, 0, g.cnt, g.e.rows > kRows};
+                ok = issue_s(cur, 0) && (!cur.two || issue_s(cur, 1));
+            }
+            while (have && ok) {
+                Tile nx = cur;
+                ++nx.T;
+                bool more = true;
+                if (cur.t + 1 < cur.cnt) {
+                    ++nx.t;
+                } else {
+                    more = walk.next(c, io, sch, g);
+                    nx.t = 0;
+                    nx.cnt = g.cnt;
+                    nx.two = g.e.rows > kRows;
+                }
+                // P V of a tile before the next S of the same rows, which overwrites that P
+                ok = issue_pv(cur, 0) && (!more || issue_s(nx, 0));
+                if (ok && cur.two) ok = issue_pv(cur, 1);
+                if (ok && more && nx.two) ok = issue_s(nx, 1);
+                cur = nx;
+                have = more;
+            }
+            // before TMEM is released every MMA must have completed, on the failure path too
+            mma_commit(bar(kBarEnd));
+            if (!mbar_wait(bar(kBarEnd), 0) || !ok) set_status(c.status, kDevTimeout);
+        }
+        __syncwarp();
+    }
+
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+}  // namespace akv

@@ -24,7 +24,7 @@ struct RopeParams {
     int on;             // 0: no rotation
     int interleaved;
     int rot;            // rotated channels, a multiple of 16
-    float amp;
+    double amp;
     double turns[kRopeMaxPairs];   // turns per position
 };
 
@@ -70,7 +70,7 @@ struct RopeLane {
 // (|x| <= pi / 4: the first terms left out are below 4e-13).  float32
 // functions lose another unit in the last place, and a key that is off by that
 // is stored under the neighbouring code more often.
-__device__ __forceinline__ void turn(int pos, double turns, float amp, float &c, float &s)
+__device__ __forceinline__ void turn(int pos, double turns, double amp, float &c, float &s)
 {
     double t = (double)pos * turns;
     t -= rint(t);

@@ -359,7 +359,7 @@ typedef enum { ATLASKV_ROPE_HALF = 0, ATLASKV_ROPE_INTERLEAVED = 1 } atlaskv_rop
 typedef struct {
     int32_t layout;                          /* atlaskv_rope_layout */
     int32_t rotary_dim;                      /* a multiple of 16, 16 <= rotary_dim <= head_dim */
-    float amplitude;                         /* finite; 1 for a plain rotation */
+    double amplitude;                        /* finite; 1 for a plain rotation */
     double freq[ATLASKV_ROPE_MAX_PAIRS];     /* radians per position of pair i < rotary_dim / 2 */
 } atlaskv_rope_spec;
 
@@ -372,7 +372,7 @@ typedef struct {
  * factor > 0, original_len >= 0 and 0 <= low_turns < high_turns are finite. */
 atlaskv_status atlaskv_rope_init(atlaskv_rope_spec *spec, int32_t layout, int32_t rotary_dim, double base,
                                  double factor, double original_len, double low_turns, double high_turns,
-                                 float amplitude);
+                                 double amplitude);
 
 typedef struct {
     int32_t dtype;             /* atlaskv_dtype of x and y */
