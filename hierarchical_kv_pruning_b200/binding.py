@@ -143,6 +143,8 @@ _lock = threading.Lock()
 def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     """Load the in-tree library (raises OSError if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -195,7 +197,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
 
 
 def _check(status: int):
-    if status != ATLASKV_OK:
+    if status:
         raise AtlaskvError(status, atlaskv_last_error())
 
 
@@ -629,27 +631,34 @@ class CsrHikvpTree:
         return atlaskv_refine_stats(self.handle)
 
 
-def _rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype):
-    """(pointer, token stride) of a token tensor [B][N][heads][D] whose token
-    rows are dense and evenly spaced, as a slice of a wider projection's is."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise AtlaskvError(ATLASKV_EINVAL, "%s: %s of shape %s, expected %s of shape %s" %
-                           (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
+# A decode step makes two of the calls below per layer, so their checks are
+# kept to a few tensor queries each.
+
+def _refuse(name: str, t: torch.Tensor, shape, dtype, what: str):
+    raise AtlaskvError(ATLASKV_EINVAL, "%s must be a %s %s tensor of shape %s, not %s of shape %s and strides %s" %
+                       (name, what, dtype, tuple(shape), t.dtype, tuple(t.shape), t.stride()))
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
+    """Token stride of a token tensor [B][N][heads][D] whose token rows are
+    dense and evenly spaced, as a slice of a wider projection's is (0: dense)."""
+    if t.dtype is not dtype or t.shape != shape:
+        _refuse(name, t, shape, dtype, "token")
     if t.is_contiguous():
-        return t.data_ptr(), shape[2] * shape[3]
+        return 0
     s0, s1, s2, s3 = t.stride()
     if shape[1] == 1:      # one token per sequence: the stride between sequences is the token stride
         s1 = s0
     if shape[0] * shape[1] == 1:
         s1 = shape[2] * shape[3]
     if s3 != 1 or (s2 != shape[3] and shape[2] > 1) or (shape[0] > 1 and s0 != shape[1] * s1):
-        raise AtlaskvError(ATLASKV_EINVAL, "%s: its tokens must be dense rows at an even stride" % name)
-    return t.data_ptr(), s1
+        _refuse(name, t, shape, dtype, "token")
+    return s1
 
 
 def _dense(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise AtlaskvError(ATLASKV_EINVAL, "%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, "contiguous")
     return t.data_ptr()
 
 
@@ -657,15 +666,15 @@ def _ints(name: str, t: Optional[torch.Tensor], shape) -> Optional[int]:
     return None if t is None else _dense(name, t, shape, torch.int32)
 
 
-def _on_device(device: torch.device, tensors, stream) -> int:
+def _on_device(index: int, stream, *tensors) -> int:
     """The stream to launch on: `stream`, or the current one of the current
     device, where every tensor has to be."""
-    if device.index != torch.cuda.current_device():
-        raise AtlaskvError(ATLASKV_EINVAL, "%s is not the current device" % device)
+    if index != torch._C._cuda_getDevice():
+        raise AtlaskvError(ATLASKV_EINVAL, "device %d is not the current device" % index)
     for t in tensors:
-        if t is not None and t.device != device:
-            raise AtlaskvError(ATLASKV_EINVAL, "a tensor on %s in a call on %s" % (t.device, device))
-    return _stream(stream)
+        if t is not None and t.get_device() != index:
+            raise AtlaskvError(ATLASKV_EINVAL, "a tensor on %s in a call on device %d" % (t.device, index))
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
 
 
 def _used_on(stream, *tensors):
@@ -690,16 +699,16 @@ def rope(x, positions, spec: Rope, out=None, backward: bool = False, stream=None
     """Rotate x [B][N][H][D] by positions [B][N] (int32) into out (a new
     tensor by default; x itself for in place).  backward=True is the transpose:
     it turns a gradient of the rotated tensor into that of the tensor."""
-    if x.dim() != 4:
-        raise AtlaskvError(ATLASKV_EINVAL, "x must be [B][N][H][D]")
-    shape, given = x.shape, out
+    shape, dtype, given = x.shape, x.dtype, out
+    if len(shape) != 4 or not x.is_cuda:
+        raise AtlaskvError(ATLASKV_EINVAL, "x must be a CUDA tensor [B][N][H][D]")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    s = _on_device(x.device, (positions, out), stream)
-    xp, xs = _rows("x", x, shape, x.dtype)
-    yp, ys = _rows("out", out, shape, x.dtype)
-    io = atlaskv_rope_io(_dtype_code(x.dtype), shape[2], shape[3], shape[0] * shape[1], xp, xs,
-                         _ints("positions", positions, shape[:2]), yp, ys, 1 if backward else 0)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    B, N, H, D = shape
+    s = _on_device(x.get_device(), stream, positions, out)
+    io = atlaskv_rope_io(_dtype_code(dtype), H, D, B * N, x.data_ptr(), _rows("x", x, shape, dtype),
+                         _dense("positions", positions, (B, N), torch.int32), out.data_ptr(),
+                         _rows("out", out, shape, dtype), 1 if backward else 0)
     atlaskv_rope(spec.spec, io, s)
     if given is None:
         _used_on(stream, out)
@@ -722,7 +731,8 @@ class KvCache:
             raise AtlaskvError(ATLASKV_EINVAL, "pages must be a uint8 [n_pages][%d] CUDA tensor" % width)
         self.pages, self.device = pages, pages.device
         d = atlaskv_cache_desc(self.n_kv_heads, self.head_dim, self.page_size, pages.shape[0], _ptr(pages))
-        self.handle = atlaskv_create_cache(d, _on_device(self.device, (), stream))
+        self._index = pages.get_device()
+        self.handle = atlaskv_create_cache(d, _on_device(self._index, stream))
 
     @staticmethod
     def page_bytes(n_kv_heads: int, head_dim: int, page_size: int) -> int:
@@ -751,10 +761,12 @@ class KvCache:
         except Exception:
             pass
 
-    def _seqs(self, N: int, block_table, kv_len, q_len) -> atlaskv_seqs:
-        B, width = block_table.shape
-        return atlaskv_seqs(B, N, width, _ints("block_table", block_table, (B, width)), _ints("kv_len", kv_len, (B,)),
-                            _ints("q_len", q_len, (B,)))
+    def _seqs(self, B: int, N: int, block_table, kv_len, q_len) -> atlaskv_seqs:
+        shape = block_table.shape
+        if len(shape) != 2 or shape[0] != B:
+            _refuse("block_table", block_table, (B, "max_pages"), torch.int32, "contiguous")
+        return atlaskv_seqs(B, N, shape[1], _dense("block_table", block_table, shape, torch.int32),
+                            _dense("kv_len", kv_len, (B,), torch.int32), _ints("q_len", q_len, (B,)))
 
     def append(self, k, v, block_table, kv_len, q_len=None, rope: Optional[Rope] = None, positions=None, q=None,
                q_out=None, stream=None):
@@ -762,24 +774,21 @@ class KvCache:
         is given, by positions [B][N] or by slot) and rotate the queries
         q [B][N][H][D] into q_out along the way.  Returns q_out (None without q)."""
         B, N = k.shape[:2]
-        given = q_out
+        dtype, given = k.dtype, q_out
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        s = _on_device(self.device, (k, v, block_table, kv_len, q_len, positions, q, q_out), stream)
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        s = _on_device(self._index, stream, k, v, block_table, kv_len, q_len, positions, q, q_out)
         shape = (B, N, self.n_kv_heads, self.head_dim)
-        kp, ks = _rows("k", k, shape, k.dtype)
-        vp, vs = _rows("v", v, shape, k.dtype)
-        qp, qs, H, qo = None, 0, 0, None
+        qp = qo = None
+        qs = H = 0
         if q is not None:
             H = q.shape[2] if q.dim() == 4 else 0
-            qp, qs = _rows("q", q, (B, N, H, self.head_dim), k.dtype)
-            qo = _dense("q_out", q_out, q.shape, k.dtype)
-        if block_table.shape[0] != B:
-            raise AtlaskvError(ATLASKV_EINVAL, "block_table has %d rows for %d sequences" % (block_table.shape[0], B))
-        io = atlaskv_append_io(_dtype_code(k.dtype), kp, vp, ks, vs, _ints("positions", positions, (B, N)), H, qp, qs,
-                               qo)
+            q_shape = (B, N, H, self.head_dim)
+            qp, qs, qo = q.data_ptr(), _rows("q", q, q_shape, dtype), _dense("q_out", q_out, q_shape, dtype)
+        io = atlaskv_append_io(_dtype_code(dtype), k.data_ptr(), v.data_ptr(), _rows("k", k, shape, dtype),
+                               _rows("v", v, shape, dtype), _ints("positions", positions, (B, N)), H, qp, qs, qo)
         atlaskv_cache_append(self.handle, None if rope is None else rope.spec,
-                             self._seqs(N, block_table, kv_len, q_len), io, s)
+                             self._seqs(B, N, block_table, kv_len, q_len), io, s)
         if q is not None and given is None:
             _used_on(stream, q_out)
         return q_out
@@ -789,15 +798,20 @@ class KvCache:
         as k, v [B][N][H_kv][D]; rows past q_len are left as they were (zero
         in tensors allocated here)."""
         shape = (block_table.shape[0], int(N), self.n_kv_heads, self.head_dim)
-        new = [k_out is None, v_out is None]
-        k_out = torch.zeros(shape, dtype=dtype, device=self.device) if k_out is None else k_out
-        v_out = torch.zeros(shape, dtype=k_out.dtype, device=self.device) if v_out is None else v_out
-        if stream is not None and any(new):   # the zeros were written on the current stream
+        new = []
+        if k_out is None:
+            k_out = torch.zeros(shape, dtype=dtype, device=self.device)
+            new.append(k_out)
+        dtype = k_out.dtype
+        if v_out is None:
+            v_out = torch.zeros(shape, dtype=dtype, device=self.device)
+            new.append(v_out)
+        if stream is not None and new:   # the zeros were written on the current stream
             stream.wait_stream(torch.cuda.current_stream())
-        s = _on_device(self.device, (block_table, kv_len, q_len, k_out, v_out), stream)
-        atlaskv_cache_read(self.handle, self._seqs(shape[1], block_table, kv_len, q_len), _dtype_code(k_out.dtype),
-                           _dense("k_out", k_out, shape, k_out.dtype), _dense("v_out", v_out, shape, k_out.dtype), s)
-        _used_on(stream, *[t for t, n in zip((k_out, v_out), new) if n])
+        s = _on_device(self._index, stream, block_table, kv_len, q_len, k_out, v_out)
+        atlaskv_cache_read(self.handle, self._seqs(shape[0], shape[1], block_table, kv_len, q_len), _dtype_code(dtype),
+                           _dense("k_out", k_out, shape, dtype), _dense("v_out", v_out, shape, dtype), s)
+        _used_on(stream, *new)
         return k_out, v_out
 
     def workspace_size(self, dtype, B: int, N: int, H: int) -> int:
@@ -807,30 +821,29 @@ class KvCache:
                stream=None):
         """Causal attention of q [B][N][H][D] over the stored sequences:
         (out, lse).  Rows past q_len are left as they were."""
-        B, N, H, D = q.shape
-        new = []
+        B, N, H, _ = q.shape
+        shape, dtype, new = (B, N, H, self.head_dim), q.dtype, []
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty(shape, dtype=dtype, device=q.device)
             new.append(out)
         if lse is None:
             lse = torch.empty((B, N, H), dtype=torch.float32, device=q.device)
             new.append(lse)
-        code = _dtype_code(q.dtype)
+        code = _dtype_code(dtype)
         if workspace is None:
             nbytes = atlaskv_cache_workspace_size(self.handle, code, B, N, H)
             workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
             new.append(workspace)
-        s = _on_device(self.device, (q, block_table, kv_len, q_len, out, lse, workspace), stream)
-        qp, qs = _rows("q", q, (B, N, H, self.head_dim), q.dtype)
-        if block_table.shape[0] != B:
-            raise AtlaskvError(ATLASKV_EINVAL, "block_table has %d rows for %d sequences" % (block_table.shape[0], B))
-        io = atlaskv_cache_attend_io(code, H, qp, qs, _dense("out", out, (B, N, H, D), q.dtype),
-                                     _dense("lse", lse, (B, N, H), torch.float32), scale)
-        atlaskv_cache_attend(self.handle, self._seqs(N, block_table, kv_len, q_len), io, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), s)
-        _used_on(stream, *new)
+        s = _on_device(self._index, stream, q, block_table, kv_len, q_len, out, lse, workspace)
+        io = atlaskv_cache_attend_io(code, H, q.data_ptr(), _rows("q", q, shape, dtype),
+                                     _dense("out", out, shape, dtype), _dense("lse", lse, (B, N, H), torch.float32),
+                                     scale)
+        atlaskv_cache_attend(self.handle, self._seqs(B, N, block_table, kv_len, q_len), io, workspace.data_ptr(),
+                             workspace.nbytes, s)
+        if new:
+            _used_on(stream, *new)
         return out, lse
 
     def sync_status(self, stream=None):
         """Raises on a device-side error of the calls so far."""
-        atlaskv_cache_sync_status(self.handle, _on_device(self.device, (), stream))
+        atlaskv_cache_sync_status(self.handle, _on_device(self._index, stream))

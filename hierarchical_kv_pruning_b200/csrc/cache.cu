@@ -116,13 +116,31 @@ int num_sms()
     return n;
 }
 
-// Rows per warp so that small calls spread over the device (one step of R
-// rows per warp) and large ones reuse a lane's cosines over many heads.
-int rows_per_warp(long long tokens, int rows, int R, int sms)
+// Launch with programmatic stream serialization (the kernel begins while the
+// one before it drains, and waits before it reads or writes).
+template <typename... KArgs, typename... Args>
+atlaskv_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Args... args)
 {
-    const long long steps = tokens * ((rows + R - 1) / R);     // warps at one step each
-    const long long per = std::max(1LL, steps / ((long long)sms * 32));
-    return (int)std::min<long long>(per * R, (rows + R - 1) / R * R);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    AKV_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return ATLASKV_OK;
+}
+
+// Tokens per CTA: whole tokens up to one batch of row slots, so that a CTA's
+// loads are all started at once.
+int tokens_per_cta(int rows, int D)
+{
+    const int slots = akv::kRowBatch * akv::kTokThreads / (D / 8);
+    return std::max(1, std::min(akv::kTokMax, slots / rows));
 }
 
 atlaskv_status check_cache(const atlaskv_cache *c)
@@ -180,25 +198,6 @@ size_t ca_workspace(const atlaskv_cache *c)
 {
     const size_t n = ca_ctas<T, D, NT>(c);
     return n * sizeof(akv::CaDesc) + n * 2 * akv::Ca<T, D, NT>::kSlot * sizeof(float);
-}
-
-// Launch with programmatic stream serialization (the kernel begins while the
-// one before it drains, and waits before it reads or writes).
-template <typename... KArgs, typename... Args>
-atlaskv_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    AKV_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
-    return ATLASKV_OK;
 }
 
 template <typename T, int D, int NT>
@@ -262,7 +261,6 @@ atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, cons
             if ((D) == 64) LAUNCH(__nv_bfloat16, 64);                                \
             else LAUNCH(__nv_bfloat16, 128);                                         \
         }                                                                            \
-        AKV_CUDA(cudaGetLastError());                                                \
     } while (0)
 
 }  // namespace
@@ -324,13 +322,11 @@ atlaskv_status atlaskv_rope(const atlaskv_rope_spec *spec, const atlaskv_rope_io
     r.ys = ys;
     r.H = io->H;
     r.backward = io->backward;
-    const int R = 32 / (io->head_dim / 8);
-    r.heads_per_warp = rows_per_warp(io->tokens, io->H, R, num_sms());
-    const long long warps = io->tokens * ((io->H + r.heads_per_warp - 1) / r.heads_per_warp);
-    const long long blocks = (warps + akv::kRopeThreads / 32 - 1) / (akv::kRopeThreads / 32);
+    r.per_cta = tokens_per_cta(io->H, io->head_dim);
+    const long long blocks = (io->tokens + r.per_cta - 1) / r.per_cta;
     AKV_RET(check_grid(blocks));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define LAUNCH(T, D) akv::rope_kernel<T, D><<<(unsigned)blocks, akv::kRopeThreads, 0, s>>>(p, r)
+#define LAUNCH(T, D) AKV_RET(launch_pdl(akv::rope_kernel<T, D>, dim3((unsigned)blocks), akv::kTokThreads, 0, s, p, r))
     AKV_TD(io->dtype, io->head_dim, LAUNCH);
 #undef LAUNCH
     return ATLASKV_OK;
@@ -434,14 +430,13 @@ atlaskv_status atlaskv_cache_append(atlaskv_cache *c, const atlaskv_rope_spec *r
     a.qs = qs;
     a.pos = io->positions;
     a.H = io->H;
-    const int R = 32 / (D / 8), rows = 2 * p.H_kv + io->H;
-    const long long tokens = (long long)p.B * p.N;
-    a.rows_per_warp = rows_per_warp(tokens, rows, R, c->num_sms);
-    const long long warps = tokens * ((rows + a.rows_per_warp - 1) / a.rows_per_warp);
-    const long long blocks = (warps + akv::kAppendThreads / 32 - 1) / (akv::kAppendThreads / 32);
+    if (2LL * p.H_kv + io->H > (1 << 20)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^20 heads");
+    a.per_cta = tokens_per_cta(2 * p.H_kv + io->H, D);
+    const long long tokens = (long long)p.B * p.N, blocks = (tokens + a.per_cta - 1) / a.per_cta;
     AKV_RET(check_grid(blocks));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define LAUNCH(T, D) akv::cache_append_kernel<T, D><<<(unsigned)blocks, akv::kAppendThreads, 0, s>>>(rp, p, a)
+#define LAUNCH(T, D) \
+    AKV_RET(launch_pdl(akv::cache_append_kernel<T, D>, dim3((unsigned)blocks), akv::kTokThreads, 0, s, rp, p, a))
     AKV_TD(io->dtype, D, LAUNCH);
 #undef LAUNCH
     return ATLASKV_OK;
@@ -456,12 +451,16 @@ atlaskv_status atlaskv_cache_read(atlaskv_cache *c, const atlaskv_seqs *seqs, in
     AKV_RET(cache_params(c, seqs, &p));
     if (!aligned16(k_out) || !aligned16(v_out)) return fail(ATLASKV_EINVAL, "k_out and v_out must be 16-byte aligned");
     if (seqs->B == 0 || (!k_out && !v_out)) return ATLASKV_OK;
-    const int D = c->d.head_dim, per_block = 8 * (32 / (D / 8));
-    const long long rows = (long long)p.B * p.N * p.H_kv, blocks = (rows + per_block - 1) / per_block;
+    const int D = c->d.head_dim;
+    const int wide = (((uintptr_t)k_out | (uintptr_t)v_out) & 31u) == 0;
+    // blocks of 16 slots that N consecutive slots can touch
+    const int per_seq = (int)std::min<long long>(((long long)p.N + 30) / 16, (long long)p.max_pages * p.page_size / 16);
+    const long long warps = (long long)p.B * per_seq * p.H_kv, blocks = (warps + akv::kReadWarps - 1) / akv::kReadWarps;
     AKV_RET(check_grid(blocks));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define LAUNCH(T, D) \
-    akv::cache_read_kernel<T, D><<<(unsigned)blocks, 256, 0, s>>>(p, static_cast<T *>(k_out), static_cast<T *>(v_out))
+#define LAUNCH(T, D)                                                                                                \
+    AKV_RET(launch_pdl(akv::cache_read_kernel<T, D>, dim3((unsigned)blocks), 32 * akv::kReadWarps, 0, s, p,         \
+                       static_cast<T *>(k_out), static_cast<T *>(v_out), per_seq, wide))
     AKV_TD(dtype, D, LAUNCH);
 #undef LAUNCH
     return ATLASKV_OK;

@@ -106,16 +106,6 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, const uint
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 
-// Two codes at bits 0..3 and 16..19 -> bf16x2 of the stored numbers.
-__device__ __forceinline__ uint32_t stored2(uint32_t x, uint32_t scale2, uint32_t low2)
-{
-    uint32_t c, r;
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(c) : "r"(x));   // (x & mask) | 128.0
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c), "r"(0x43004300u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(scale2), "r"(low2));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -31,6 +31,8 @@
 // Every wait is bounded; one that gives up sets ETIMEOUT in the status word.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_attend.cuh"
 
 namespace akv {
@@ -42,7 +44,7 @@ constexpr int kRows = 128, kBlockRows = 256, kKeys = 128, kHalf = 64;
 constexpr int kKV = 2, kRaw = 3;    // stages of the K and V tiles, of the codes
 constexpr int kThreads = 512;
 constexpr int kDequantWarp = 8, kMmaWarp = 12, kCopyWarp = 13;
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;   // 2 x 128 x (192 + 64) = the 512 x 128 of the launch
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;   // 2 x 128 x (168 + 88) = the 512 x 128 of the launch
 constexpr float kRescale = 8.f;     // rescale O when a row's maximum grows by more than 2^8
 // A partial costs about this many units to write, read and join.
 constexpr int kPartialUnits = 6;
@@ -72,6 +74,68 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// tcgen05.mma with the operand descriptors as their low words (start address in
+// 16-byte units, lbo) plus a constant step: the steps of a tile then need two
+// registers and no 64-bit sums, which the compiler would keep 32 of.
+template <int StepA, int StepB>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u32 x, %1, %6;\n\tadd.u32 y, %2, %7;\n\t"
+        "mov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc), "n"(StepA), "n"(StepB));
+}
+
+template <int StepA, int StepB>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u32 x, %1, %6;\n\tadd.u32 y, %2, %7;\n\t"
+        "mov.b64 b, {y, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, {%8, %8, %8, %8}, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc), "n"(StepA), "n"(StepB), "r"(0u));
+}
+
+// f(integral constant 0 .. N - 1)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void steps(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        steps<N, I + 1>(f);
+    }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
 }
 
 // An entry: 256-row block rb of sequence b (for every KV head).
@@ -333,12 +397,14 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                 float mx[8];
                 load_s(kHalf);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = sc[j];
+                for (int j = 0; j < 8; ++j) mx[j] = max3(sc[j], sc[j + 8], sc[j + 16]);
 #pragma unroll
-                for (int j = 8; j < kHalf; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
+                for (int j = 24; j < 56; j += 2) mx[(j >> 1) & 7] = max3(mx[(j >> 1) & 7], sc[j], sc[j + 1]);
+#pragma unroll
+                for (int j = 56; j < kHalf; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
                 load_s(0);
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
+                for (int j = 0; j < kHalf; j += 2) mx[(j >> 1) & 7] = max3(mx[(j >> 1) & 7], sc[j], sc[j + 1]);
                 const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                 const float m_new = fmaxf(m, top * io.scale_log2);
@@ -365,7 +431,10 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                     }
                 }
                 const float neg = m == -INFINITY ? 0.f : -m;
-                float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                float2 ps[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ps[j] = make_float2(0.f, 0.f);
+                const float2 sc2 = make_float2(io.scale_log2, io.scale_log2), neg2 = make_float2(neg, neg);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (half == 1) load_s(kHalf);   // P so far lies over keys 0 .. 31 of S
@@ -374,15 +443,17 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            const float e0 = fast_exp2(fmaf(sc[k + j], io.scale_log2, neg));
-                            const float e1 = fast_exp2(fmaf(sc[k + j + 1], io.scale_log2, neg));
-                            ps[(j >> 1) & 7] += e0 + e1;
-                            pk[j / 2] = pack_bf16(e0, e1);
+                            float2 x = fma2(make_float2(sc[k + j], sc[k + j + 1]), sc2, neg2);
+                            x.x = fast_exp2(x.x);
+                            x.y = fast_exp2(x.y);
+                            ps[(j >> 1) & 3] = add2(ps[(j >> 1) & 3], x);
+                            pk[j / 2] = pack_bf16(x.x, x.y);
                         }
                         tmem_st16(tS + (half * kHalf + k) / 2, pk);
                     }
                 }
-                l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+                const float2 pt = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+                l += pt.x + pt.y;
                 tmem_wait_st();
                 fence_before_sync();
                 __syncwarp();
@@ -456,77 +527,79 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             for (int t = 0; t < g.cnt; ++t, ++T) {
                 const int st = T % kKV;
                 const int key0 = (g.k0 + t) * kKeys;
-                if (T >= kKV) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarKEmpty + st), ((T / kKV) + 1) & 1));
+                // the two halves' stages of the ring
+                const int r0 = (2 * T) % kRaw, r1 = (2 * T + 1) % kRaw;
+                failed = !mbar_wait(bar(kBarRawFull + r0), (2 * T / kRaw) & 1) ||
+                         !mbar_wait(bar(kBarRawFull + r1), ((2 * T + 1) / kRaw) & 1) ||
+                         (T >= kKV && !mbar_wait(bar(kBarKEmpty + st), ((T / kKV) + 1) & 1));
+                failed = __any_sync(0xffffffffu, failed);
                 if (failed) break;
-                // keys of both halves, then values
-#pragma unroll 1
-                for (int step = 0; step < 4; ++step) {
-                    const int h = step & 1, raw = 2 * T + h, rs = raw % kRaw;
-                    const bool is_v = step >= 2;
-                    if (!is_v) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarRawFull + rs), (raw / kRaw) & 1));
-                    else if (h == 0 && T >= kKV)
-                        failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarVEmpty + st), ((T / kKV) + 1) & 1));
-                    if (failed) break;
-                    const uint8_t *blk = ctc_smem + SM::kOffR + rs * SM::kR + (key >> 4) * B::kBytes;
-                    const int tok = key & 15, r = h * kHalf + key;
-                    const bool ok = key0 + r < g.e.s.kv;
-                    uint8_t *tile = ctc_smem + (is_v ? SM::kOffV : SM::kOffK) + st * SM::kT;
-                    // this thread's D / 2 channels: D / 64 groups of 32
+                const bool tail = key0 + kKeys > g.e.s.kv;   // tokens past the sequence become zeros
+                // 32 channels (group gr of the row) of token `key` of half h: 4 chunks of 16 bytes
+                auto put = [&](uint8_t *tile, int h, int gr, const uint32_t *w, uint32_t s2, uint32_t m2) {
+                    const bool zero = tail && key0 + h * kHalf + key >= g.e.s.kv;
+                    uint8_t *dst = tile + (gr >> 1) * (kKeys * 128) + (h * kHalf + key) * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 v;
+                        v.x = stored2(w[i], s2, m2);
+                        v.y = stored2(w[i] >> 4, s2, m2);
+                        v.z = stored2(w[i] >> 8, s2, m2);
+                        v.w = stored2(w[i] >> 12, s2, m2);
+                        if (zero) v = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(dst + ((((gr & 1) * 4 + i) ^ (key & 7)) << 4)) = v;
+                    }
+                };
+                const int tok = key & 15;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *blk = ctc_smem + SM::kOffR + (h ? r1 : r0) * SM::kR + (key >> 4) * B::kBytes;
 #pragma unroll
                     for (int gi = 0; gi < kBlocks; ++gi) {
-                        const int gr = col * kBlocks + gi;   // group of the row
-                        uint32_t w[4], s2, m2;
-                        if (is_v) {
-                            const uint8_t *p = blk + B::v_scale(tok, gr);
-                            s2 = *reinterpret_cast<const uint16_t *>(p);
-                            m2 = *reinterpret_cast<const uint16_t *>(p + 4);
-                            s2 |= s2 << 16;
-                            m2 |= m2 << 16;
-                            if constexpr (D == 128) {
-                                const uint2 a = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr));
-                                const uint2 e = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr + 1));
-                                w[0] = a.x;
-                                w[1] = a.y;
-                                w[2] = e.x;
-                                w[3] = e.y;
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w[i] = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(tok, 4 * gr + i));
-                            }
-                        } else {
-                            const uint32_t pr = *reinterpret_cast<const uint32_t *>(blk + B::k_pair(tok, gr));
-                            s2 = prmt(pr, pr, 0x1010);
-                            m2 = prmt(pr, pr, 0x3232);
-                            const uint4 a = *reinterpret_cast<const uint4 *>(blk + B::k_codes(tok) + gr * 16);
-                            w[0] = a.x;
-                            w[1] = a.y;
-                            w[2] = a.z;
-                            w[3] = a.w;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int ch = gr * 4 + i;   // 8-channel chunk of the row
-                            uint4 v;
-                            v.x = stored2(w[i], s2, m2);
-                            v.y = stored2(w[i] >> 4, s2, m2);
-                            v.z = stored2(w[i] >> 8, s2, m2);
-                            v.w = stored2(w[i] >> 12, s2, m2);
-                            if (!ok) v = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(tile + (ch >> 3) * (kKeys * 128) + sw128(r, ch & 7)) = v;
-                        }
-                    }
-                    if (is_v) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kBarRawEmpty + rs));
-                    }
-                    if (h == 1) {
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
+                        const int gr = col * kBlocks + gi;
+                        const uint32_t pr = *reinterpret_cast<const uint32_t *>(blk + B::k_pair(tok, gr));
+                        const uint4 a = *reinterpret_cast<const uint4 *>(blk + B::k_codes(tok) + gr * 16);
+                        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                        put(ctc_smem + SM::kOffK + st * SM::kT, h, gr, w, prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232));
                     }
                 }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarKFull + st));
+                if (T >= kKV) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarVEmpty + st), ((T / kKV) + 1) & 1));
                 if (failed) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *blk = ctc_smem + SM::kOffR + (h ? r1 : r0) * SM::kR + (key >> 4) * B::kBytes;
+#pragma unroll
+                    for (int gi = 0; gi < kBlocks; ++gi) {
+                        const int gr = col * kBlocks + gi;
+                        const uint8_t *p = blk + B::v_scale(tok, gr);
+                        const uint32_t s1 = *reinterpret_cast<const uint16_t *>(p);
+                        const uint32_t m1 = *reinterpret_cast<const uint16_t *>(p + 4);
+                        uint32_t w[4];
+                        if constexpr (D == 128) {
+                            const uint2 a = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr));
+                            const uint2 e = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr + 1));
+                            w[0] = a.x;
+                            w[1] = a.y;
+                            w[2] = e.x;
+                            w[3] = e.y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                w[i] = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(tok, 4 * gr + i));
+                        }
+                        put(ctc_smem + SM::kOffV + st * SM::kT, h, gr, w, s1 | s1 << 16, m1 | m1 << 16);
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(kBarVFull + st));
+                    mbar_arrive(bar(kBarRawEmpty + r0));
+                    mbar_arrive(bar(kBarRawEmpty + r1));
+                }
             }
         }
         if (failed && lane == 0) set_status(c.status, kDevTimeout);
@@ -571,8 +644,10 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
         } else if (warp == kMmaWarp && lane == 0) {
             // ================= MMA issue: one thread =================
             const uint32_t idesc_s = make_idesc(kRows, kKeys, 0, 0), idesc_o = make_idesc(kRows, D, 0, 1);
-            const uint64_t dq0 = make_desc(sb + SM::kOffQ, 16, 1024), dk0 = make_desc(sb + SM::kOffK, 16, 1024),
-                           dv0 = make_desc(sb + SM::kOffV, kKeys * 128, 1024);
+            const uint64_t dq = make_desc(sb + SM::kOffQ, 16, 1024), dk = make_desc(sb + SM::kOffK, 16, 1024),
+                           dv = make_desc(sb + SM::kOffV, kKeys * 128, 1024);
+            const uint32_t hi = (uint32_t)(dq >> 32);   // the same of all three
+            const uint32_t dq0 = (uint32_t)dq, dk0 = (uint32_t)dk, dv0 = (uint32_t)dv;
             struct Tile {
                 int T, t, cnt;      // running count; index in its stretch and the stretch's tiles
                 bool two;           // both row tiles have rows
@@ -586,12 +661,13 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                     ++Sg[grp];
                 }
                 fence_after_sync();
-                const uint64_t q = dq0 + (uint64_t)((grp * SM::kQ) >> 4), k = dk0 + (uint64_t)(((x.T % kKV) * SM::kT) >> 4);
+                const uint32_t q = dq0 + ((grp * SM::kQ) >> 4), k = dk0 + (((x.T % kKV) * SM::kT) >> 4);
                 const uint32_t td = tmem + SM::kColS + grp * kKeys;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16(td, q + (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4),
-                             k + (uint64_t)(((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+                steps<D / 16>([&](auto i) {
+                    constexpr int ks = i, a = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
+                                  b = ((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) / 16;
+                    mma_ss<a, b>(td, q, k, hi, idesc_s, ks > 0 ? 1u : 0u);
+                });
                 mma_commit(bar(kBarS + grp));
                 if (grp == 1 || !x.two) mma_commit(bar(kBarKEmpty + x.T % kKV));
                 return true;
@@ -604,12 +680,12 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                 const int sn = Sg[grp] - 1;
                 if (x.t == 0 && sn > 0 && !mbar_wait(bar(kBarDrained + grp), (sn - 1) & 1)) return false;
                 fence_after_sync();
-                const uint64_t v = dv0 + (uint64_t)(((x.T % kKV) * SM::kT) >> 4);
+                const uint32_t v = dv0 + (((x.T % kKV) * SM::kT) >> 4);
                 const uint32_t ta = tmem + SM::kColS + grp * kKeys, td = tmem + SM::kColO + grp * D;
-#pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    mma_bf16_ts(td, ta + 8 * ks, v + (uint64_t)((ks * 16 * 128) >> 4), idesc_o,
-                                (x.t > 0 || ks > 0) ? 1u : 0u);
+                steps<kKeys / 16>([&](auto i) {
+                    constexpr int ks = i;
+                    mma_ts<8 * ks, ks * 128>(td, ta, v, hi, idesc_o, (x.t > 0 || ks > 0) ? 1u : 0u);
+                });
                 if (x.t == x.cnt - 1) mma_commit(bar(kBarO + grp));
                 if (grp == 1 || !x.two) mma_commit(bar(kBarVEmpty + x.T % kKV));
                 return true;

@@ -110,21 +110,29 @@ __device__ __forceinline__ uint32_t quantise8(float *x, __nv_bfloat16 &scale, __
         s = 0.f;
         scale = __float2bfloat16(0.f);
     }
+    // The nearest code without a division: round (x - m) times 1 / s, which is at most one off, then decide by the
+    // exact remainder.  bfloat16 input lies on the border of two codes often, and then goes to the even one.
+    const float inv = s > 0.f ? __frcp_rn(s) : 0.f, half = 0.5f * s;
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float t = s > 0.f ? rintf(__fdiv_rn(x[e] - m, s)) : 0.f;
-        w |= (uint32_t)(int)fminf(fmaxf(t, 0.f), 15.f) << (4 * e);
+        const float d = x[e] - m, c = rintf(d * inv), r = fmaf(-c, s, d);
+        int i = (int)c;
+        const bool odd = i & 1;
+        i += (r > half || (r == half && odd)) ? 1 : (r < -half || (r == -half && odd)) ? -1 : 0;
+        w |= (s > 0.f ? (uint32_t)min(max(i, 0), 15) : 0u) << (4 * e);
     }
     return w;
 }
 
-// bf16(low + c scale) of the 8 codes of a word.
-__device__ __forceinline__ void stored8(uint32_t w, __nv_bfloat16 scale, __nv_bfloat16 low, float *x)
+// Two codes at bits 0..3 and 16..19 -> bf16x2 of the stored numbers.
+__device__ __forceinline__ uint32_t stored2(uint32_t x, uint32_t scale2, uint32_t low2)
 {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = __bfloat162float(__hfma(__float2bfloat16((float)((w >> (4 * e)) & 15u)), scale, low));
+    uint32_t c, r;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(c) : "r"(x));   // (x & mask) | 128.0
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c), "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(scale2), "r"(low2));
+    return r;
 }
 
 struct AppendIo {
@@ -132,72 +140,102 @@ struct AppendIo {
     void *q_out;
     long long ks, vs, qs;       // token strides in elements
     const int32_t *pos;         // rotary positions or null
-    int H, rows_per_warp;       // query heads (0: none); rows of a token per warp
+    int H, per_cta;             // query heads (0: none); tokens per CTA
 };
 
-constexpr int kAppendThreads = 256;
-
-// A token's rows are its H_kv keys, its H_kv values and its H queries; a warp
-// takes rows_per_warp of them.
+// A token's rows are its H_kv keys, its H_kv values and its H queries; a CTA
+// takes whole tokens, like rope_kernel.  HBM bounds it for many tokens: most
+// of the bytes are the queries'.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kTokThreads)
     cache_append_kernel(const __grid_constant__ RopeParams p, const CacheParams c, const AppendIo io)
 {
-    constexpr int L = D / 8, R = 32 / L;
+    constexpr int L = D / 8, R = kTokThreads / L;
     using B = Blk<D>;
-    __shared__ double turns[kRopeMaxPairs];
-    rope_turns(p, turns);
-    const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-    const int rows = 2 * c.H_kv + io.H, parts = (rows + io.rows_per_warp - 1) / io.rows_per_warp;
-    const long long w = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-    if (w >= (long long)c.B * c.N * parts) return;
-    const long long tok = w / parts;
-    const int b = (int)(tok / c.N), n = (int)(tok - (long long)b * c.N);
-    const Seq s = load_seq(c, b);
-    if (n >= s.q) return;
-    const int slot = s.kv - s.q + n;
-    if (slot < 0) {
-        set_status(c.status, kDevBadPage);
-        return;
-    }
-    const int page = c.table[(size_t)b * c.max_pages + slot / c.page_size];
-    const RopeLane r = rope_lane(p, turns, j, io.pos ? io.pos[tok] : slot, false);
-    const int r0 = (int)(w - tok * parts) * io.rows_per_warp, r1 = min(rows, r0 + io.rows_per_warp);
-    bool bad = false;
-    for (int i = r0; i < r1; i += R) {
-        const int row = i + sub;
-        const bool ok = row < r1, is_k = row < c.H_kv, is_q = row >= 2 * c.H_kv;
-        const int h = is_k ? row : is_q ? row - 2 * c.H_kv : row - c.H_kv;
-        const T *src = is_k   ? reinterpret_cast<const T *>(io.k) + tok * io.ks
-                       : is_q ? reinterpret_cast<const T *>(io.q) + tok * io.qs
-                              : reinterpret_cast<const T *>(io.v) + tok * io.vs;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8];
-        if (ok) load8<T>(src + (size_t)h * D + 8 * j, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e];
-        rope_apply(p, r, sub * L, y);
-        if (is_k || is_q) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e];
+    __shared__ RopeTable table;
+    __shared__ int s_slot[kTokMax], s_page[kTokMax];   // a token's slot (-1: not stored) and page
+    const int row = threadIdx.x / L, j = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L;
+    const long long t0 = (long long)blockIdx.x * io.per_cta;
+    const int n = (int)min((long long)io.per_cta, (long long)c.B * c.N - t0), rows = 2 * c.H_kv + io.H, slots = n * rows;
+    griddep_wait();
+    if (threadIdx.x < n) {
+        const long long tok = t0 + threadIdx.x;
+        const int b = (int)(tok / c.N), i = (int)(tok - (long long)b * c.N);
+        const Seq s = load_seq(c, b);
+        int slot = -1, page = 0;
+        if (i < s.q) {
+            slot = s.kv - s.q + i;
+            if (slot < 0) {
+                set_status(c.status, kDevBadPage);
+                slot = -1;
+            } else {
+                page = c.table[(size_t)b * c.max_pages + slot / c.page_size];
+            }
         }
-        if (ok && is_q) store8<T>(reinterpret_cast<T *>(io.q_out) + ((size_t)tok * io.H + h) * D + 8 * j, x);
-        if (__any_sync(0xffffffffu, ok && !is_q)) {   // keys or values among the warp's rows
-            __nv_bfloat16 scale, low;
-            bool nf = false;
-            const uint32_t code = quantise8(x, scale, low, nf);
-            if (ok && !is_q) {
-                bad |= nf;
-                uint8_t *blk = block_at<D>(c, page, h, slot);
-                const int t = slot & 15;
-                if (blk && is_k) {
-                    *reinterpret_cast<uint32_t *>(blk + B::k_codes(t) + 4 * j) = code;
-                    if (j % 4 == 0)
-                        *reinterpret_cast<__nv_bfloat162 *>(blk + B::k_pair(t, j / 4)) = __nv_bfloat162(scale, low);
-                } else if (blk) {
-                    *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 64 * j / D) + (D == 128 ? (j & 1) * 4 : 0)) = code;
-                    if (j % 4 == 0) {
-                        *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4)) = scale;
-                        *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4) + 4) = low;
+        s_slot[threadIdx.x] = slot;
+        s_page[threadIdx.x] = page;
+    }
+    __syncthreads();
+    bool bad = false;
+    for (int base = 0; base < slots; base += kRowBatch * R) {   // CTA-uniform
+        float x[kRowBatch][8];
+        int tok[kRowBatch], at[kRowBatch];                      // at: row of the token, -1: nothing to do
+#pragma unroll
+        for (int k = 0; k < kRowBatch; ++k) {
+            const int i = base + k * R + row;
+            tok[k] = i < slots ? i / rows : 0;
+            at[k] = i < slots && s_slot[tok[k]] >= 0 ? i - tok[k] * rows : -1;
+            if (at[k] >= 0) {
+                const int h = at[k];
+                const T *src = h < c.H_kv       ? reinterpret_cast<const T *>(io.k) + (t0 + tok[k]) * io.ks + (size_t)h * D
+                               : h < 2 * c.H_kv ? reinterpret_cast<const T *>(io.v) + (t0 + tok[k]) * io.vs +
+                                                      (size_t)(h - c.H_kv) * D
+                                                : reinterpret_cast<const T *>(io.q) + (t0 + tok[k]) * io.qs +
+                                                      (size_t)(h - 2 * c.H_kv) * D;
+                load8<T>(src + 8 * j, x[k]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+            }
+        }
+        if (base == 0 && p.on) {
+            rope_fill(p, table, n, 1.f, [&](int i) { return io.pos ? io.pos[t0 + i] : s_slot[i]; });
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kRowBatch; ++k) {
+            const bool is_q = at[k] >= 2 * c.H_kv, is_v = at[k] >= c.H_kv && !is_q, is_k = at[k] >= 0 && at[k] < c.H_kv;
+            if (p.on) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = x[k][e];
+                rope_apply(p, table, tok[k], j, row0, y);
+                if (!is_v) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[k][e] = y[e];
+                }
+            }
+            if (is_q)
+                store8<T>(reinterpret_cast<T *>(io.q_out) + ((size_t)(t0 + tok[k]) * io.H + at[k] - 2 * c.H_kv) * D + 8 * j,
+                          x[k]);
+            if (__any_sync(0xffffffffu, is_k || is_v)) {
+                __nv_bfloat16 scale, low;
+                bool nf = false;
+                const uint32_t code = quantise8(x[k], scale, low, nf);
+                if (is_k || is_v) {
+                    bad |= nf;
+                    const int slot = s_slot[tok[k]], t = slot & 15;
+                    uint8_t *blk = block_at<D>(c, s_page[tok[k]], is_k ? at[k] : at[k] - c.H_kv, slot);
+                    if (blk && is_k) {
+                        *reinterpret_cast<uint32_t *>(blk + B::k_codes(t) + 4 * j) = code;
+                        if (j % 4 == 0)
+                            *reinterpret_cast<__nv_bfloat162 *>(blk + B::k_pair(t, j / 4)) = __nv_bfloat162(scale, low);
+                    } else if (blk) {
+                        *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 64 * j / D) + (D == 128 ? (j & 1) * 4 : 0)) = code;
+                        if (j % 4 == 0) {
+                            *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4)) = scale;
+                            *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4) + 4) = low;
+                        }
                     }
                 }
             }
@@ -206,39 +244,114 @@ __global__ void __launch_bounds__(kAppendThreads)
     if (bad) set_status(c.status, kDevNonFinite);
 }
 
-// A warp reads the key and the value rows of one (token, KV head) per row slot.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheParams c, T *k_out, T *v_out)
+// 32 bytes of an output row: one store when the tensors allow it (wide: 32-byte aligned).
+__device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide)
 {
-    constexpr int L = D / 8, R = 32 / L;
-    using B = Blk<D>;
-    const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-    const long long row = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * R + sub;
-    if (row >= (long long)c.B * c.N * c.H_kv) return;
-    const int h = (int)(row % c.H_kv);
-    const long long tok = row / c.H_kv;
-    const int b = (int)(tok / c.N), n = (int)(tok - (long long)b * c.N);
-    const Seq s = load_seq(c, b);
-    if (n >= s.q) return;
-    const int slot = s.kv - s.q + n;
-    if (slot < 0) {
-        set_status(c.status, kDevBadPage);
+    if (!wide) {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         return;
     }
-    const uint8_t *blk = block_at<D>(c, c.table[(size_t)b * c.max_pages + slot / c.page_size], h, slot);
-    if (!blk) return;
-    const int t = slot & 15;
-    float x[8];
-    if (k_out) {
-        const __nv_bfloat162 pr = *reinterpret_cast<const __nv_bfloat162 *>(blk + B::k_pair(t, j / 4));
-        stored8(*reinterpret_cast<const uint32_t *>(blk + B::k_codes(t) + 4 * j), pr.x, pr.y, x);
-        store8<T>(k_out + (size_t)row * D + 8 * j, x);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// bf16 pairs (channel 2 i, 2 i + 1) of the 8 codes of a word.
+__device__ __forceinline__ void stored8(uint32_t w, uint32_t scale2, uint32_t low2, uint32_t *out)
+{
+    uint32_t v[4];   // channels (i, i + 4)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = stored2(w >> (4 * i), scale2, low2);
+    out[0] = __byte_perm(v[0], v[1], 0x5410);
+    out[1] = __byte_perm(v[2], v[3], 0x5410);
+    out[2] = __byte_perm(v[0], v[1], 0x7632);
+    out[3] = __byte_perm(v[2], v[3], 0x7632);
+}
+
+// 16 channels given as 8 bf16 pairs into an output row.
+template <typename T>
+__device__ __forceinline__ void store16(T *p, const uint32_t *w, bool wide)
+{
+    if constexpr (sizeof(T) == 2) {
+        store32(p, w, wide);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = w[4 * k + i] << 16;
+                f[2 * i + 1] = w[4 * k + i] & 0xffff0000u;
+            }
+            store32(p + 8 * k, f, wide);
+        }
     }
-    if (v_out) {
-        const __nv_bfloat16 *pr = reinterpret_cast<const __nv_bfloat16 *>(blk + B::v_scale(t, j / 4));
-        stored8(*reinterpret_cast<const uint32_t *>(blk + B::v_codes(t, 64 * j / D) + (D == 128 ? (j & 1) * 4 : 0)),
-                pr[0], pr[2], x);
-        store8<T>(v_out + (size_t)row * D + 8 * j, x);
+}
+
+// A warp reads one block (16 slots of a KV head) of a sequence: HBM bounds it,
+// so all of the block's loads are started before the first code is turned into
+// a number, and a lane writes whole 32-byte sectors.  Slots that the call does
+// not read are skipped at the stores.
+constexpr int kReadWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const CacheParams c, T *k_out, T *v_out, int blocks, int wide)
+{
+    constexpr int L = D / 16, R = 32 / L, P = 16 / R;   // lanes per row (16 channels each), rows per step, steps
+    using B = Blk<D>;
+    griddep_wait();
+    const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
+    const long long w = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5);   // (sequence, block, KV head)
+    if (w >= (long long)c.B * blocks * c.H_kv) return;
+    const int h = (int)(w % c.H_kv);
+    const long long x = w / c.H_kv;
+    const int b = (int)(x / blocks), i = (int)(x - (long long)b * blocks);
+    const Seq s = load_seq(c, b);
+    if (s.kv < s.q) set_status(c.status, kDevBadPage);   // tokens below slot 0
+    const int first = s.kv - s.q, slot0 = (max(first, 0) & ~15) + 16 * i;
+    if (slot0 >= s.kv || s.q == 0) return;
+    const uint8_t *blk = block_at<D>(c, c.table[(size_t)b * c.max_pages + slot0 / c.page_size], h, slot0);
+    if (!blk) return;
+    const int g = j / 2;   // 16 channels lie in one group of 32
+    uint2 kc[P], vc[P];
+    uint32_t kp[P], vs[P], vm[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const int t = k * R + sub;
+        if (k_out) {
+            kc[k] = *reinterpret_cast<const uint2 *>(blk + B::k_codes(t) + 8 * j);
+            kp[k] = *reinterpret_cast<const uint32_t *>(blk + B::k_pair(t, g));
+        }
+        if (v_out) {
+            if constexpr (D == 128) {
+                vc[k] = *reinterpret_cast<const uint2 *>(blk + B::v_codes(t, j));
+            } else {
+                vc[k].x = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(t, 2 * j));
+                vc[k].y = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(t, 2 * j + 1));
+            }
+            vs[k] = *reinterpret_cast<const uint16_t *>(blk + B::v_scale(t, g));
+            vm[k] = *reinterpret_cast<const uint16_t *>(blk + B::v_scale(t, g) + 4);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const int slot = slot0 + k * R + sub;
+        if (slot < first || slot >= s.kv) continue;
+        const size_t at = (((size_t)b * c.N + slot - first) * c.H_kv + h) * D + 16 * j;
+        uint32_t out[8];
+        if (k_out) {
+            const uint32_t s2 = __byte_perm(kp[k], kp[k], 0x1010), m2 = __byte_perm(kp[k], kp[k], 0x3232);
+            stored8(kc[k].x, s2, m2, out);
+            stored8(kc[k].y, s2, m2, out + 4);
+            store16<T>(k_out + at, out, wide);
+        }
+        if (v_out) {
+            const uint32_t s2 = vs[k] | vs[k] << 16, m2 = vm[k] | vm[k] << 16;
+            stored8(vc[k].x, s2, m2, out);
+            stored8(vc[k].y, s2, m2, out + 4);
+            store16<T>(v_out + at, out, wide);
+        }
     }
 }
 

@@ -8,10 +8,12 @@
 // per position, minus its nearest integer: exact to 2^-53 of the product), so
 // cos and sin are float32-accurate at any int32 position.
 //
-// A lane owns 8 consecutive channels of a row ("chunk"), D / 8 lanes per row,
+// HBM bounds it for many tokens, latency for few.  A CTA takes whole tokens
+// (one, or several when their heads are few): it starts the loads, computes
+// each token's rot / 2 angles once into shared memory, then turns the rows.  A
+// lane owns 8 consecutive channels of a row ("chunk"), D / 8 lanes per row,
 // 2 or 4 rows per warp; the partner channels of the half layout live in
-// another lane of the row and come by shuffle.  The lane's 8 (half) or 4
-// (interleaved) cosines serve every head that its warp visits.
+// another lane of the row and come by shuffle.
 #pragma once
 
 #include "common.cuh"
@@ -56,15 +58,6 @@ template <> __device__ __forceinline__ void store8<float>(float *p, const float 
     *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// A lane's cosines and sines (times the amplitude) for chunk j of a row at
-// `pos`: entry e belongs to channel 8 j + e (half) or to channels 8 j + 2 e,
-// 8 j + 2 e + 1 (interleaved, e < 4).
-struct RopeLane {
-    float c[8], s[8];
-    int partner;       // half layout: lane offset within the row of the partner chunk
-    bool first, active;
-};
-
 // cos and sin of `t` turns, |t| <= 1/2, times amp, each rounded once to
 // float32: the Taylor series on an eighth of a turn around the nearest quarter
 // (|x| <= pi / 4: the first terms left out are below 4e-13).  float32
@@ -94,53 +87,61 @@ __device__ __forceinline__ void turn(int pos, double turns, double amp, float &c
     s = q == 0 ? fs : q == 1 ? fc : q == 2 ? -fs : -fc;
 }
 
-__device__ __forceinline__ RopeLane rope_lane(const RopeParams &p, const double *turns, int j, int pos, bool backward)
+constexpr int kTokThreads = 256;   // of the kernels below and of the cache's append
+constexpr int kTokMax = 32;        // tokens per CTA at most
+
+// The cosines and sines of `n` tokens' pairs: pos(i) is token i's position.
+struct RopeTable {
+    float c[kTokMax * kRopeMaxPairs], s[kTokMax * kRopeMaxPairs];
+};
+template <typename F>
+__device__ __forceinline__ void rope_fill(const RopeParams &p, RopeTable &t, int n, float sign, F &&pos)
 {
-    RopeLane r;
-    r.active = p.on && 8 * j < p.rot;
-    r.partner = j;
-    r.first = true;
-    if (!r.active) return r;
-    const int hc = p.rot / 16;   // chunks of one half
-    r.first = j < hc;
-    r.partner = p.interleaved ? j : r.first ? j + hc : j - hc;
-    const int base = p.interleaved ? 4 * j : 8 * (r.first ? j : j - hc);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (e >= 4 && p.interleaved) break;
-        turn(pos, turns[base + e], p.amp, r.c[e], r.s[e]);
-        if (backward) r.s[e] = -r.s[e];
+    const int pairs = p.rot / 2;   // 8 .. 64
+    for (int i = threadIdx.x; i < n * pairs; i += kTokThreads) {
+        const int tok = i / pairs, e = i - tok * pairs;
+        float c, s;
+        turn(pos(tok), p.turns[e], p.amp, c, s);
+        t.c[tok * kRopeMaxPairs + e] = c;
+        t.s[tok * kRopeMaxPairs + e] = sign * s;
     }
-    return r;
 }
 
-// Rotate the lane's 8 channels in place.  All 32 lanes call it (shuffles);
-// row0: the row's first lane.
-__device__ __forceinline__ void rope_apply(const RopeParams &p, const RopeLane &r, int row0, float *x)
+// Rotate a lane's 8 channels (chunk j of a row of token slot tok) in place.
+// All 32 lanes call it (shuffles); row0: the row's first lane.
+__device__ __forceinline__ void rope_apply(const RopeParams &p, const RopeTable &t, int tok, int j, int row0, float *x)
 {
-    if (!p.on) return;
+    const bool active = 8 * j < p.rot;
     if (p.interleaved) {
-        if (!r.active) return;
+        if (!active) return;
+        const float4 c = *reinterpret_cast<const float4 *>(&t.c[tok * kRopeMaxPairs + 4 * j]);
+        const float4 s = *reinterpret_cast<const float4 *>(&t.s[tok * kRopeMaxPairs + 4 * j]);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float u = x[2 * e], v = x[2 * e + 1];
-            x[2 * e] = fmaf(u, r.c[e], -v * r.s[e]);
-            x[2 * e + 1] = fmaf(v, r.c[e], u * r.s[e]);
+            x[2 * e] = fmaf(u, cc[e], -v * ss[e]);
+            x[2 * e + 1] = fmaf(v, cc[e], u * ss[e]);
         }
         return;
     }
+    const int hc = p.rot / 16;   // chunks of one half
+    const bool first = j < hc;
+    const int partner = !active ? j : first ? j + hc : j - hc, at = tok * kRopeMaxPairs + 8 * (first ? j : j - hc);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, x[e], row0 + r.partner);
-        if (r.active) x[e] = fmaf(x[e], r.c[e], r.first ? -o * r.s[e] : o * r.s[e]);
+    for (int e = 0; e < 8; e += 4) {
+        float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (active) {
+            c = *reinterpret_cast<const float4 *>(&t.c[at + e]);
+            s = *reinterpret_cast<const float4 *>(&t.s[at + e]);
+        }
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float o = __shfl_sync(0xffffffffu, x[e + i], row0 + partner);
+            if (active) x[e + i] = fmaf(x[e + i], cc[i], first ? -o * ss[i] : o * ss[i]);
+        }
     }
-}
-
-// The spec's turns in shared memory (a lane's index into them is its own).
-__device__ __forceinline__ void rope_turns(const RopeParams &p, double *sm)
-{
-    if (p.on && threadIdx.x < kRopeMaxPairs) sm[threadIdx.x] = p.turns[threadIdx.x];
-    __syncthreads();
 }
 
 struct RopeIo {
@@ -148,34 +149,45 @@ struct RopeIo {
     void *y;
     const int32_t *pos;
     long long tokens, xs, ys;   // strides in elements
-    int H, heads_per_warp, backward;
+    int H, per_cta, backward;   // heads; tokens per CTA
 };
 
-constexpr int kRopeThreads = 256;
+// Row slots (token, head) of the CTA's tokens, kRowBatch passes of loads at a time.
+constexpr int kRowBatch = 2;
 
-// A warp takes one token's heads_per_warp heads (a multiple of the rows per
-// warp, the last group ragged).
 template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p, const RopeIo io)
+__global__ void __launch_bounds__(kTokThreads) rope_kernel(const __grid_constant__ RopeParams p, const RopeIo io)
 {
-    constexpr int L = D / 8, R = 32 / L;   // lanes per row, rows per warp
-    __shared__ double turns[kRopeMaxPairs];
-    rope_turns(p, turns);
-    const int lane = threadIdx.x & 31, j = lane % L, sub = lane / L;
-    const int parts = (io.H + io.heads_per_warp - 1) / io.heads_per_warp;
-    const long long w = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    if (w >= io.tokens * parts) return;
-    const long long tok = w / parts;
-    const int h0 = (int)(w - tok * parts) * io.heads_per_warp, h1 = min(io.H, h0 + io.heads_per_warp);
-    const T *x = reinterpret_cast<const T *>(io.x) + tok * io.xs + 8 * j;
-    T *y = reinterpret_cast<T *>(io.y) + tok * io.ys + 8 * j;
-    const RopeLane r = rope_lane(p, turns, j, io.pos[tok], io.backward != 0);
-    for (int h = h0; h < h1; h += R) {   // warp-uniform
-        const bool ok = h + sub < h1;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (ok) load8<T>(x + (size_t)(h + sub) * D, v);
-        rope_apply(p, r, sub * L, v);
-        if (ok) store8<T>(y + (size_t)(h + sub) * D, v);
+    constexpr int L = D / 8, R = kTokThreads / L;   // lanes per row, rows per pass
+    __shared__ RopeTable table;
+    const int row = threadIdx.x / L, j = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L;
+    const long long t0 = (long long)blockIdx.x * io.per_cta;
+    const int n = (int)min((long long)io.per_cta, io.tokens - t0), slots = n * io.H;
+    griddep_wait();
+    for (int base = 0; base < slots; base += kRowBatch * R) {   // CTA-uniform
+        float x[kRowBatch][8];
+        int tok[kRowBatch], h[kRowBatch];
+#pragma unroll
+        for (int k = 0; k < kRowBatch; ++k) {
+            const int i = base + k * R + row;
+            tok[k] = i < slots ? i / io.H : 0;
+            h[k] = i < slots ? i - tok[k] * io.H : -1;
+            if (h[k] >= 0)
+                load8<T>(reinterpret_cast<const T *>(io.x) + (t0 + tok[k]) * io.xs + (size_t)h[k] * D + 8 * j, x[k]);
+            else
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+        }
+        if (base == 0) {
+            rope_fill(p, table, n, io.backward ? -1.f : 1.f, [&](int i) { return io.pos[t0 + i]; });
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kRowBatch; ++k) {
+            rope_apply(p, table, tok[k], j, row0, x[k]);
+            if (h[k] >= 0)
+                store8<T>(reinterpret_cast<T *>(io.y) + (t0 + tok[k]) * io.ys + (size_t)h[k] * D + 8 * j, x[k]);
+        }
     }
 }
 

@@ -205,7 +205,7 @@ def test_read_whole_histories(D, H_kv, P, lens, dtype):
         k, v = cache.read(N, table.cuda(), i32(lens), i32(lens), dtype=dtype)
         cache.sync_status()
         only = torch.full_like(k, 7.)
-        binding.atlaskv_cache_read(cache.handle, cache._seqs(N, table.cuda(), i32(lens), i32(lens)),
+        binding.atlaskv_cache_read(cache.handle, cache._seqs(len(lens), N, table.cuda(), i32(lens), i32(lens)),
                                    binding._dtype_code(dtype), None, only.data_ptr(),
                                    torch.cuda.current_stream().cuda_stream)
         torch.cuda.synchronize()
@@ -214,6 +214,24 @@ def test_read_whole_histories(D, H_kv, P, lens, dtype):
         assert torch.equal(k[b, :n].cpu().to(F64), wk) and torch.equal(v[b, :n].cpu().to(F64), wv)
         assert bool((k[b, n:] == 0).all()) and bool((only[b, n:] == 7).all())
         assert torch.equal(only[b, :n], v[b, :n])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_read_into_tensors_on_16_byte_boundaries(dtype):
+    D, H_kv, P, lens, N = 128, 2, 32, [40, 7], 9
+    pool = ref.Pool(6, H_kv, D, P)
+    table = tables(lens, P, 6, 4)
+    for b, n in enumerate(lens):
+        pool.fill(table[b], n, seed=b)
+    size = 2 * N * H_kv * D
+    with new_cache(pool) as cache:
+        want = cache.read(N, table.cuda(), i32(lens), i32([9, 5]), dtype=dtype)
+        step = 16 // dtype.itemsize
+        raw = [torch.zeros(size + step, dtype=dtype, device="cuda")[step:].view(2, N, H_kv, D) for _ in range(2)]
+        assert raw[0].data_ptr() % 32 == 16
+        got = cache.read(N, table.cuda(), i32(lens), i32([9, 5]), k_out=raw[0], v_out=raw[1])
+        cache.sync_status()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 def test_stored_extremes():
