@@ -136,11 +136,12 @@ atlaskv_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned block, s
 }
 
 // Tokens per CTA: whole tokens up to one batch of row slots, so that a CTA's
-// loads are all started at once.
-int tokens_per_cta(int rows, int D)
+// loads are all started at once; fewer in calls too small to fill the device.
+int tokens_per_cta(long long tokens, int rows, int D, int sms)
 {
-    const int slots = akv::kRowBatch * akv::kTokThreads / (D / 8);
-    return std::max(1, std::min(akv::kTokMax, slots / rows));
+    const int slots = akv::kRowBatch * akv::kTokThreads / (D / 16);
+    const long long spread = (tokens + 4LL * sms - 1) / (4LL * sms);
+    return (int)std::max(1LL, std::min({(long long)akv::kTokMax, (long long)slots / rows, spread}));
 }
 
 atlaskv_status check_cache(const atlaskv_cache *c)
@@ -322,7 +323,7 @@ atlaskv_status atlaskv_rope(const atlaskv_rope_spec *spec, const atlaskv_rope_io
     r.ys = ys;
     r.H = io->H;
     r.backward = io->backward;
-    r.per_cta = tokens_per_cta(io->H, io->head_dim);
+    r.per_cta = tokens_per_cta(io->tokens, io->H, io->head_dim, num_sms());
     const long long blocks = (io->tokens + r.per_cta - 1) / r.per_cta;
     AKV_RET(check_grid(blocks));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -431,8 +432,9 @@ atlaskv_status atlaskv_cache_append(atlaskv_cache *c, const atlaskv_rope_spec *r
     a.pos = io->positions;
     a.H = io->H;
     if (2LL * p.H_kv + io->H > (1 << 20)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^20 heads");
-    a.per_cta = tokens_per_cta(2 * p.H_kv + io->H, D);
-    const long long tokens = (long long)p.B * p.N, blocks = (tokens + a.per_cta - 1) / a.per_cta;
+    const long long tokens = (long long)p.B * p.N;
+    a.per_cta = tokens_per_cta(tokens, 2 * p.H_kv + io->H, D, c->num_sms);
+    const long long blocks = (tokens + a.per_cta - 1) / a.per_cta;
     AKV_RET(check_grid(blocks));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 #define LAUNCH(T, D) \

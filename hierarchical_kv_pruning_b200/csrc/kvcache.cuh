@@ -89,13 +89,24 @@ constexpr float kMinScale = 7.888609052210118e-31f;     // 2^-100
 // (all lanes of the warp call it).  Returns the 8 codes, channel e at bits 4 e.
 __device__ __forceinline__ uint32_t quantise8(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad)
 {
-    float lo = INFINITY, hi = -INFINITY;
+    // 0 x is NaN for an infinity or NaN and 0 else
+    float odd = 0.f, lo = x[0], hi = x[0];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        if (!(fabsf(x[e]) <= 3.402823466e38f)) bad = true;   // infinity or NaN
-        x[e] = isnan(x[e]) ? 0.f : fminf(fmaxf(x[e], -kMaxStored), kMaxStored);
+        odd = fmaf(0.f, x[e], odd);
         lo = fminf(lo, x[e]);
         hi = fmaxf(hi, x[e]);
+    }
+    if (!(odd == 0.f && lo >= -kMaxStored && hi <= kMaxStored)) {   // hardly ever
+        lo = INFINITY;
+        hi = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            bad |= !(fabsf(x[e]) <= 3.402823466e38f);   // infinity or NaN
+            x[e] = isnan(x[e]) ? 0.f : fminf(fmaxf(x[e], -kMaxStored), kMaxStored);
+            lo = fminf(lo, x[e]);
+            hi = fmaxf(hi, x[e]);
+        }
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
@@ -105,24 +116,27 @@ __device__ __forceinline__ uint32_t quantise8(float *x, __nv_bfloat16 &scale, __
     low = __float2bfloat16_rd(lo);
     const float m = __bfloat162float(low);
     scale = __float2bfloat16_ru(__fdiv_rn(hi - m, 15.f));
-    float s = __bfloat162float(scale);
+    const float s = __bfloat162float(scale);
     if (s < kMinScale) {
-        s = 0.f;
         scale = __float2bfloat16(0.f);
+        return 0u;
     }
-    // The nearest code without a division: round (x - m) times 1 / s, which is at most one off, then decide by the
-    // exact remainder.  bfloat16 input lies on the border of two codes often, and then goes to the even one.
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f, half = 0.5f * s;
+    // The nearest code without a division or a conversion: adding 1.5 2^23 rounds (x - m) / s, which is at most one off,
+    // into the low bits, then the exact remainder decides.  bfloat16 input lies on the border of two codes often,
+    // and then goes to the even one: the remainder must reach half a step from an odd code and pass it from an even one.
+    const float inv = __frcp_rn(s);
+    const int half = __float_as_int(0.5f * s);
     uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float d = x[e] - m, c = rintf(d * inv), r = fmaf(-c, s, d);
-        int i = (int)c;
-        const bool odd = i & 1;
-        i += (r > half || (r == half && odd)) ? 1 : (r < -half || (r == -half && odd)) ? -1 : 0;
-        w |= (s > 0.f ? (uint32_t)min(max(i, 0), 15) : 0u) << (4 * e);
+    for (int e = 7; e >= 0; --e) {
+        const float d = x[e] - m, t = fmaf(d, inv, 12582912.f), r = fmaf(-(t - 12582912.f), s, d);
+        int i = __float_as_int(t);
+        const float h = __int_as_float(half + 1 - (i & 1));
+        i += r >= h ? 1 : 0;
+        i -= r <= -h ? 1 : 0;
+        w = 16u * w + (uint32_t)i;   // the 2^22 of the constants overflow away, except the last one's
     }
-    return w;
+    return w - 0x4b400000u * 0x11111111u;
 }
 
 // Two codes at bits 0..3 and 16..19 -> bf16x2 of the stored numbers.
@@ -143,20 +157,21 @@ struct AppendIo {
     int H, per_cta;             // query heads (0: none); tokens per CTA
 };
 
-// A token's rows are its H_kv keys, its H_kv values and its H queries; a CTA
-// takes whole tokens, like rope_kernel.  HBM bounds it for many tokens: most
-// of the bytes are the queries'.
+// A CTA takes whole tokens, like rope_kernel: their keys and values (a row is
+// 16 or 8 lanes of 8 channels, so that 4 lanes are a group), then the queries.
+// HBM bounds it for many tokens, most of the bytes are the queries'; close to
+// it the rounding to codes, about 20 instructions a number.
 template <typename T, int D>
-__global__ void __launch_bounds__(kTokThreads)
+__global__ void __launch_bounds__(kTokThreads, 4)
     cache_append_kernel(const __grid_constant__ RopeParams p, const CacheParams c, const AppendIo io)
 {
-    constexpr int L = D / 8, R = kTokThreads / L;
+    constexpr int L = D / 8, R = kTokThreads / L;   // lanes per row, rows per pass
     using B = Blk<D>;
     __shared__ RopeTable table;
     __shared__ int s_slot[kTokMax], s_page[kTokMax];   // a token's slot (-1: not stored) and page
-    const int row = threadIdx.x / L, j = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L;
+    const int j = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L;
     const long long t0 = (long long)blockIdx.x * io.per_cta;
-    const int n = (int)min((long long)io.per_cta, (long long)c.B * c.N - t0), rows = 2 * c.H_kv + io.H, slots = n * rows;
+    const int n = (int)min((long long)io.per_cta, (long long)c.B * c.N - t0), rows = 2 * c.H_kv;
     griddep_wait();
     if (threadIdx.x < n) {
         const long long tok = t0 + threadIdx.x;
@@ -176,72 +191,87 @@ __global__ void __launch_bounds__(kTokThreads)
         s_page[threadIdx.x] = page;
     }
     __syncthreads();
+    if (p.on) rope_fill(p, table, n, 1.f, [&](int i) { return io.pos ? io.pos[t0 + i] : s_slot[i]; });
+
+    // keys and values: the rows of the next pass are loaded before this one's are stored
     bool bad = false;
-    for (int base = 0; base < slots; base += kRowBatch * R) {   // CTA-uniform
-        float x[kRowBatch][8];
-        int tok[kRowBatch], at[kRowBatch];                      // at: row of the token, -1: nothing to do
-#pragma unroll
-        for (int k = 0; k < kRowBatch; ++k) {
-            const int i = base + k * R + row;
-            tok[k] = i < slots ? i / rows : 0;
-            at[k] = i < slots && s_slot[tok[k]] >= 0 ? i - tok[k] * rows : -1;
-            if (at[k] >= 0) {
-                const int h = at[k];
-                const T *src = h < c.H_kv       ? reinterpret_cast<const T *>(io.k) + (t0 + tok[k]) * io.ks + (size_t)h * D
-                               : h < 2 * c.H_kv ? reinterpret_cast<const T *>(io.v) + (t0 + tok[k]) * io.vs +
-                                                      (size_t)(h - c.H_kv) * D
-                                                : reinterpret_cast<const T *>(io.q) + (t0 + tok[k]) * io.qs +
-                                                      (size_t)(h - 2 * c.H_kv) * D;
-                load8<T>(src + 8 * j, x[k]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-            }
+    int tok = 0, h = threadIdx.x / L;
+    auto wrap = [&](int &t, int &hh) {
+        while (hh >= rows) {
+            hh -= rows;
+            ++t;
         }
-        if (base == 0 && p.on) {
-            rope_fill(p, table, n, 1.f, [&](int i) { return io.pos ? io.pos[t0 + i] : s_slot[i]; });
-            __syncthreads();
-        }
+    };
+    auto load = [&](int t, int hh, Raw8<T> &raw) {
+        if (t >= n || s_slot[t] < 0) return;
+        const T *src = hh < c.H_kv ? reinterpret_cast<const T *>(io.k) + (t0 + t) * io.ks + hh * D
+                                   : reinterpret_cast<const T *>(io.v) + (t0 + t) * io.vs + (hh - c.H_kv) * D;
+        raw.load(src + 8 * j);
+    };
+    wrap(tok, h);
+    Raw8<T> raw, next;
+    load(tok, h, raw);
+    if (p.on) __syncthreads();
+    const int hc = p.rot / 16;   // chunks of a half
+    for (int base = 0; base < n * rows; base += R) {   // CTA-uniform
+        int t2 = tok, h2 = h + R;
+        wrap(t2, h2);
+        load(t2, h2, next);
+        const int slot = tok < n ? s_slot[tok] : -1;
+        const bool is_k = slot >= 0 && h < c.H_kv, ok = slot >= 0;
+        float x[8];
+        raw.widen(x);
+        if (p.on && __any_sync(0xffffffffu, is_k)) {
+            const float *tc = table.c + (ok ? tok : 0) * kRopeMaxPairs, *ts = table.s + (ok ? tok : 0) * kRopeMaxPairs;
+            if (p.interleaved) {
+                if (is_k && 8 * j < p.rot) {
 #pragma unroll
-        for (int k = 0; k < kRowBatch; ++k) {
-            const bool is_q = at[k] >= 2 * c.H_kv, is_v = at[k] >= c.H_kv && !is_q, is_k = at[k] >= 0 && at[k] < c.H_kv;
-            if (p.on) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[k][e];
-                rope_apply(p, table, tok[k], j, row0, y);
-                if (!is_v) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[k][e] = y[e];
-                }
-            }
-            if (is_q)
-                store8<T>(reinterpret_cast<T *>(io.q_out) + ((size_t)(t0 + tok[k]) * io.H + at[k] - 2 * c.H_kv) * D + 8 * j,
-                          x[k]);
-            if (__any_sync(0xffffffffu, is_k || is_v)) {
-                __nv_bfloat16 scale, low;
-                bool nf = false;
-                const uint32_t code = quantise8(x[k], scale, low, nf);
-                if (is_k || is_v) {
-                    bad |= nf;
-                    const int slot = s_slot[tok[k]], t = slot & 15;
-                    uint8_t *blk = block_at<D>(c, s_page[tok[k]], is_k ? at[k] : at[k] - c.H_kv, slot);
-                    if (blk && is_k) {
-                        *reinterpret_cast<uint32_t *>(blk + B::k_codes(t) + 4 * j) = code;
-                        if (j % 4 == 0)
-                            *reinterpret_cast<__nv_bfloat162 *>(blk + B::k_pair(t, j / 4)) = __nv_bfloat162(scale, low);
-                    } else if (blk) {
-                        *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 64 * j / D) + (D == 128 ? (j & 1) * 4 : 0)) = code;
-                        if (j % 4 == 0) {
-                            *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4)) = scale;
-                            *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4) + 4) = low;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float u = x[2 * e], v = x[2 * e + 1], cc = tc[4 * j + e], ss = ts[4 * j + e];
+                        x[2 * e] = fmaf(u, cc, -v * ss);
+                        x[2 * e + 1] = fmaf(v, cc, u * ss);
                     }
                 }
+            } else {   // the partner chunk is another lane's
+                const bool first = j < hc, active = is_k && 8 * j < p.rot;
+                const int partner = row0 + (8 * j >= p.rot ? j : first ? j + hc : j - hc);
+                tc += 8 * (first ? j : j - hc);
+                ts += 8 * (first ? j : j - hc);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float o = __shfl_sync(0xffffffffu, x[e], partner);
+                    if (active) x[e] = fmaf(x[e], tc[e], first ? -o * ts[e] : o * ts[e]);
+                }
             }
         }
+        __nv_bfloat16 scale, low;
+        bool nf = false;
+        const uint32_t code = quantise8(x, scale, low, nf);
+        if (ok) {
+            bad |= nf;
+            const int t = slot & 15;
+            uint8_t *blk = block_at<D>(c, s_page[tok], is_k ? h : h - c.H_kv, slot);
+            if (blk && is_k) {
+                *reinterpret_cast<uint32_t *>(blk + B::k_codes(t) + 4 * j) = code;
+                if (j % 4 == 0) *reinterpret_cast<__nv_bfloat162 *>(blk + B::k_pair(t, j / 4)) = __nv_bfloat162(scale, low);
+            } else if (blk) {
+                *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 64 * j / D) + (D == 128 ? (j & 1) * 4 : 0)) = code;
+                if (j % 4 == 0) {
+                    *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4)) = scale;
+                    *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4) + 4) = low;
+                }
+            }
+        }
+        raw = next;
+        tok = t2;
+        h = h2;
     }
     if (bad) set_status(c.status, kDevNonFinite);
+    if (io.H > 0)
+        rope_rows<T, D>(
+            p, table, reinterpret_cast<const T *>(io.q) + t0 * io.qs, io.qs,
+            reinterpret_cast<T *>(io.q_out) + t0 * io.H * D, (long long)io.H * D, n, io.H, [] {},
+            [&](int t) { return s_slot[t] >= 0; });
 }
 
 // 32 bytes of an output row: one store when the tensors allow it (wide: 32-byte aligned).

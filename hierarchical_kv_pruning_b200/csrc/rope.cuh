@@ -11,9 +11,8 @@
 // HBM bounds it for many tokens, latency for few.  A CTA takes whole tokens
 // (one, or several when their heads are few): it starts the loads, computes
 // each token's rot / 2 angles once into shared memory, then turns the rows.  A
-// lane owns 8 consecutive channels of a row ("chunk"), D / 8 lanes per row,
-// 2 or 4 rows per warp; the partner channels of the half layout live in
-// another lane of the row and come by shuffle.
+// lane owns two chunks of 8 consecutive channels of a row (D / 16 lanes per
+// row): in the half layout the two whose channels are partners.
 #pragma once
 
 #include "common.cuh"
@@ -30,7 +29,20 @@ struct RopeParams {
     double turns[kRopeMaxPairs];   // turns per position
 };
 
-// 8 channels in registers <-> memory, 16-byte accesses.
+// 8 channels in registers <-> memory, 16-byte accesses: as stored, and widened.
+template <typename T> struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void widen(float *x) const
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) Vec16<T>::unpack(v[i], x + i * Vec16<T>::E);
+    }
+};
 template <typename T> __device__ __forceinline__ void load8(const T *p, float *x);
 template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float *x)
 {
@@ -107,39 +119,103 @@ __device__ __forceinline__ void rope_fill(const RopeParams &p, RopeTable &t, int
     }
 }
 
-// Rotate a lane's 8 channels (chunk j of a row of token slot tok) in place.
-// All 32 lanes call it (shuffles); row0: the row's first lane.
-__device__ __forceinline__ void rope_apply(const RopeParams &p, const RopeTable &t, int tok, int j, int row0, float *x)
+// The two chunks of lane l of a row's D / 16 lanes.
+__device__ __forceinline__ void rope_chunks(const RopeParams &p, int l, int &a, int &b)
 {
-    const bool active = 8 * j < p.rot;
-    if (p.interleaved) {
-        if (!active) return;
-        const float4 c = *reinterpret_cast<const float4 *>(&t.c[tok * kRopeMaxPairs + 4 * j]);
-        const float4 s = *reinterpret_cast<const float4 *>(&t.s[tok * kRopeMaxPairs + 4 * j]);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float u = x[2 * e], v = x[2 * e + 1];
-            x[2 * e] = fmaf(u, cc[e], -v * ss[e]);
-            x[2 * e + 1] = fmaf(v, cc[e], u * ss[e]);
-        }
-        return;
-    }
     const int hc = p.rot / 16;   // chunks of one half
-    const bool first = j < hc;
-    const int partner = !active ? j : first ? j + hc : j - hc, at = tok * kRopeMaxPairs + 8 * (first ? j : j - hc);
+    if (p.interleaved || l >= hc) {   // behind the halves: two that pass through
+        a = 2 * l;
+        b = a + 1;
+    } else {
+        a = l;
+        b = l + hc;
+    }
+}
+
+// Rotate a lane's two chunks in place.
+__device__ __forceinline__ void rope_apply(const RopeParams &p, const RopeTable &t, int tok, int l, float *a, float *b)
+{
+    const float *tc = t.c + tok * kRopeMaxPairs, *ts = t.s + tok * kRopeMaxPairs;
+    if (16 * l >= p.rot) return;   // in either layout the first rot / 16 lanes rotate
+    // half: pairs 8 l + e of (a[e], b[e]); interleaved: pairs 8 l + i of (a[2 i], a[2 i + 1]), 8 l + 4 + i of b's
+    float c[8], s[8];
 #pragma unroll
     for (int e = 0; e < 8; e += 4) {
-        float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (active) {
-            c = *reinterpret_cast<const float4 *>(&t.c[at + e]);
-            s = *reinterpret_cast<const float4 *>(&t.s[at + e]);
-        }
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(tc + 8 * l + e);
+        *reinterpret_cast<float4 *>(s + e) = *reinterpret_cast<const float4 *>(ts + 8 * l + e);
+    }
+    if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float o = __shfl_sync(0xffffffffu, x[e + i], row0 + partner);
-            if (active) x[e + i] = fmaf(x[e + i], cc[i], first ? -o * ss[i] : o * ss[i]);
+            const float u = a[2 * i], v = a[2 * i + 1], x = b[2 * i], y = b[2 * i + 1];
+            a[2 * i] = fmaf(u, c[i], -v * s[i]);
+            a[2 * i + 1] = fmaf(v, c[i], u * s[i]);
+            b[2 * i] = fmaf(x, c[4 + i], -y * s[4 + i]);
+            b[2 * i + 1] = fmaf(y, c[4 + i], x * s[4 + i]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float u = a[e], v = b[e];
+            a[e] = fmaf(u, c[e], -v * s[e]);
+            b[e] = fmaf(v, c[e], u * s[e]);
+        }
+    }
+}
+
+// Rows (token, head) of n tokens from x to y, kRowBatch passes of loads at a
+// time (kept as stored: widened they would halve the rows in flight).  begin()
+// runs once, between the first loads and the first use of the table; a token
+// is skipped where use(token) is false.
+constexpr int kRowBatch = 2;
+
+template <typename T, int D, typename Begin, typename Use>
+__device__ __forceinline__ void rope_rows(const RopeParams &p, const RopeTable &table, const T *x, long long xs, T *y,
+                                          long long ys, int n, int H, Begin &&begin, Use &&use)
+{
+    constexpr int L = D / 16, R = kTokThreads / L;   // lanes per row, rows per pass
+    const int l = threadIdx.x % L;
+    int ca, cb;
+    rope_chunks(p, l, ca, cb);
+    int tok = 0, h = threadIdx.x / L;   // this lane's row
+    auto wrap = [&](int &t, int &hh) {
+        while (hh >= H) {
+            hh -= H;
+            ++t;
+        }
+    };
+    wrap(tok, h);
+    bool started = false;
+    for (int base = 0; base < n * H; base += kRowBatch * R) {   // CTA-uniform
+        Raw8<T> ra[kRowBatch], rb[kRowBatch];
+        int t2 = tok, h2 = h;
+#pragma unroll
+        for (int k = 0; k < kRowBatch; ++k) {
+            if (t2 < n && use(t2)) {
+                const T *src = x + t2 * xs + h2 * D;
+                ra[k].load(src + 8 * ca);
+                rb[k].load(src + 8 * cb);
+            }
+            h2 += R;
+            wrap(t2, h2);
+        }
+        if (!started) {
+            begin();
+            started = true;
+        }
+#pragma unroll
+        for (int k = 0; k < kRowBatch; ++k) {
+            if (tok < n && use(tok)) {
+                float a[8], b[8];
+                ra[k].widen(a);
+                rb[k].widen(b);
+                if (p.on) rope_apply(p, table, tok, l, a, b);
+                T *dst = y + tok * ys + h * D;
+                store8<T>(dst + 8 * ca, a);
+                store8<T>(dst + 8 * cb, b);
+            }
+            h += R;
+            wrap(tok, h);
         }
     }
 }
@@ -152,43 +228,21 @@ struct RopeIo {
     int H, per_cta, backward;   // heads; tokens per CTA
 };
 
-// Row slots (token, head) of the CTA's tokens, kRowBatch passes of loads at a time.
-constexpr int kRowBatch = 2;
-
 template <typename T, int D>
-__global__ void __launch_bounds__(kTokThreads) rope_kernel(const __grid_constant__ RopeParams p, const RopeIo io)
+__global__ void __launch_bounds__(kTokThreads, 4) rope_kernel(const __grid_constant__ RopeParams p, const RopeIo io)
 {
-    constexpr int L = D / 8, R = kTokThreads / L;   // lanes per row, rows per pass
     __shared__ RopeTable table;
-    const int row = threadIdx.x / L, j = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L;
     const long long t0 = (long long)blockIdx.x * io.per_cta;
-    const int n = (int)min((long long)io.per_cta, io.tokens - t0), slots = n * io.H;
+    const int n = (int)min((long long)io.per_cta, io.tokens - t0);
     griddep_wait();
-    for (int base = 0; base < slots; base += kRowBatch * R) {   // CTA-uniform
-        float x[kRowBatch][8];
-        int tok[kRowBatch], h[kRowBatch];
-#pragma unroll
-        for (int k = 0; k < kRowBatch; ++k) {
-            const int i = base + k * R + row;
-            tok[k] = i < slots ? i / io.H : 0;
-            h[k] = i < slots ? i - tok[k] * io.H : -1;
-            if (h[k] >= 0)
-                load8<T>(reinterpret_cast<const T *>(io.x) + (t0 + tok[k]) * io.xs + (size_t)h[k] * D + 8 * j, x[k]);
-            else
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-        }
-        if (base == 0) {
+    rope_rows<T, D>(
+        p, table, reinterpret_cast<const T *>(io.x) + t0 * io.xs, io.xs, reinterpret_cast<T *>(io.y) + t0 * io.ys, io.ys, n,
+        io.H,
+        [&] {
             rope_fill(p, table, n, io.backward ? -1.f : 1.f, [&](int i) { return io.pos[t0 + i]; });
             __syncthreads();
-        }
-#pragma unroll
-        for (int k = 0; k < kRowBatch; ++k) {
-            rope_apply(p, table, tok[k], j, row0, x[k]);
-            if (h[k] >= 0)
-                store8<T>(reinterpret_cast<T *>(io.y) + (t0 + tok[k]) * io.ys + (size_t)h[k] * D + 8 * j, x[k]);
-        }
-    }
+        },
+        [](int) { return true; });
 }
 
 }  // namespace akv
