@@ -433,10 +433,13 @@ atlaskv_status atlaskv_cache_append(atlaskv_cache *c, const atlaskv_rope_spec *r
     a.H = io->H;
     if (2LL * p.H_kv + io->H > (1 << 20)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^20 heads");
     const long long tokens = (long long)p.B * p.N;
-    a.per_cta = tokens_per_cta(tokens, 2 * p.H_kv + io->H, D, c->num_sms);
-    const long long blocks = (tokens + a.per_cta - 1) / a.per_cta;
+    a.kv_per = tokens_per_cta(tokens, 2 * p.H_kv, D, c->num_sms);
+    a.q_per = io->H > 0 ? tokens_per_cta(tokens, io->H, D, c->num_sms) : 1;
+    const long long kv_ctas = (tokens + a.kv_per - 1) / a.kv_per;
+    const long long blocks = kv_ctas + (io->H > 0 ? (tokens + a.q_per - 1) / a.q_per : 0);
     AKV_RET(check_grid(blocks));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.kv_ctas = (int)kv_ctas;
 #define LAUNCH(T, D) \
     AKV_RET(launch_pdl(akv::cache_append_kernel<T, D>, dim3((unsigned)blocks), akv::kTokThreads, 0, s, rp, p, a))
     AKV_TD(io->dtype, D, LAUNCH);

@@ -85,58 +85,59 @@ __device__ __forceinline__ uint8_t *block_at(const CacheParams &c, int page, int
 constexpr float kMaxStored = 1.329227995784916e36f;     // 2^120
 constexpr float kMinScale = 7.888609052210118e-31f;     // 2^-100
 
-// Quantise the lane's 8 channels; the 32-channel group is 4 consecutive lanes
-// (all lanes of the warp call it).  Returns the 8 codes, channel e at bits 4 e.
-__device__ __forceinline__ uint32_t quantise8(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad)
+// Quantise the lane's 16 channels; the 32-channel group is 2 neighbouring lanes
+// (all lanes of the warp call it).  The codes of channels 0 .. 7 and 8 .. 15 as
+// two words, channel e at bits 4 e.
+__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad)
 {
     // 0 x is NaN for an infinity or NaN and 0 else
-    float odd = 0.f, lo = x[0], hi = x[0];
+    float2 z = make_float2(0.f, 0.f);
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        odd = fmaf(0.f, x[e], odd);
-        lo = fminf(lo, x[e]);
-        hi = fmaxf(hi, x[e]);
+    for (int e = 0; e < 16; e += 2) {
+        z = fma2(make_float2(x[e], x[e + 1]), make_float2(0.f, 0.f), z);
+        lo = min3(lo, x[e], x[e + 1]);
+        hi = max3(hi, x[e], x[e + 1]);
     }
-    if (!(odd == 0.f && lo >= -kMaxStored && hi <= kMaxStored)) {   // hardly ever
+    if (!(z.x + z.y == 0.f && lo >= -kMaxStored && hi <= kMaxStored)) {   // hardly ever
         lo = INFINITY;
         hi = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 16; ++e) {
             bad |= !(fabsf(x[e]) <= 3.402823466e38f);   // infinity or NaN
             x[e] = isnan(x[e]) ? 0.f : fminf(fmaxf(x[e], -kMaxStored), kMaxStored);
             lo = fminf(lo, x[e]);
             hi = fmaxf(hi, x[e]);
         }
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     low = __float2bfloat16_rd(lo);
     const float m = __bfloat162float(low);
     scale = __float2bfloat16_ru(__fdiv_rn(hi - m, 15.f));
     const float s = __bfloat162float(scale);
     if (s < kMinScale) {
         scale = __float2bfloat16(0.f);
-        return 0u;
+        return make_uint2(0u, 0u);
     }
-    // The nearest code without a division or a conversion: adding 1.5 2^23 rounds (x - m) / s, which is at most one off,
-    // into the low bits, then the exact remainder decides.  bfloat16 input lies on the border of two codes often,
-    // and then goes to the even one: the remainder must reach half a step from an odd code and pass it from an even one.
+    // The nearest code of (x - m) / s without a division or a conversion.  The quotient times the rounded reciprocal,
+    // corrected by its remainder, is the correctly rounded quotient (Markstein); adding 1.5 2^23 rounds that to
+    // an integer in the low bits, borders (frequent in bfloat16 input) to the even code.
     const float inv = __frcp_rn(s);
-    const int half = __float_as_int(0.5f * s);
-    uint32_t w = 0;
+    const float2 inv2 = make_float2(inv, inv), ns2 = make_float2(-s, -s), nm2 = make_float2(-m, -m),
+                 magic = make_float2(12582912.f, 12582912.f);
+    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-        const float d = x[e] - m, t = fmaf(d, inv, 12582912.f), r = fmaf(-(t - 12582912.f), s, d);
-        int i = __float_as_int(t);
-        const float h = __int_as_float(half + 1 - (i & 1));
-        i += r >= h ? 1 : 0;
-        i -= r <= -h ? 1 : 0;
-        w = 16u * w + (uint32_t)i;   // the 2^22 of the constants overflow away, except the last one's
+    for (int e = 14; e >= 0; e -= 2) {
+        const float2 d = add2(make_float2(x[e], x[e + 1]), nm2);
+        float2 q = mul2(d, inv2);
+        q = fma2(fma2(ns2, q, d), inv2, q);
+        q = add2(q, magic);
+        // the bits of 1.5 2^23 are taken off at the end, modulo 2^32
+        w[e >> 3] = 16u * w[e >> 3] + __float_as_uint(q.y);
+        w[e >> 3] = 16u * w[e >> 3] + __float_as_uint(q.x);
     }
-    return w - 0x4b400000u * 0x11111111u;
+    return make_uint2(w[0] - 0x4b400000u * 0x11111111u, w[1] - 0x4b400000u * 0x11111111u);
 }
 
 // Two codes at bits 0..3 and 16..19 -> bf16x2 of the stored numbers.
@@ -154,46 +155,65 @@ struct AppendIo {
     void *q_out;
     long long ks, vs, qs;       // token strides in elements
     const int32_t *pos;         // rotary positions or null
-    int H, per_cta;             // query heads (0: none); tokens per CTA
+    int H;                      // query heads (0: none)
+    int kv_ctas, kv_per, q_per; // CTAs of the keys and values; tokens per CTA of either kind
 };
 
-// A CTA takes whole tokens, like rope_kernel: their keys and values (a row is
-// 16 or 8 lanes of 8 channels, so that 4 lanes are a group), then the queries.
-// HBM bounds it for many tokens, most of the bytes are the queries'; close to
-// it the rounding to codes, about 20 instructions a number.
+// kv_ctas of the CTAs store keys and values, the others turn queries; both
+// take whole tokens, like rope_kernel, start their loads, find the tokens'
+// slots, fill the table and go through the rows.  Most of the bytes are the
+// queries', but the rounding to codes, about 15 instructions a number, takes
+// as long: side by side the one's memory time hides the other's issue slots
+// (the same CTA doing one after the other measured 51 us where this takes 33,
+// 5.3k tokens of 32 + 2 x 8 heads).
 template <typename T, int D>
 __global__ void __launch_bounds__(kTokThreads, 4)
     cache_append_kernel(const __grid_constant__ RopeParams p, const CacheParams c, const AppendIo io)
 {
-    constexpr int L = D / 8, R = kTokThreads / L;   // lanes per row, rows per pass
+    constexpr int L = D / 16, R = kTokThreads / L;   // lanes per row (16 consecutive channels each), rows per pass
     using B = Blk<D>;
     __shared__ RopeTable table;
-    __shared__ int s_slot[kTokMax], s_page[kTokMax];   // a token's slot (-1: not stored) and page
-    const int j = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L;
-    const long long t0 = (long long)blockIdx.x * io.per_cta;
-    const int n = (int)min((long long)io.per_cta, (long long)c.B * c.N - t0), rows = 2 * c.H_kv;
+    __shared__ int s_slot[kTokMax], s_page[kTokMax];   // a token's slot (-1: not there) and page
+    // the two kinds of CTAs evenly mixed over the grid
+    const int kv_at = (int)((long long)blockIdx.x * io.kv_ctas / gridDim.x);
+    const bool is_q = kv_at == (int)((blockIdx.x + 1LL) * io.kv_ctas / gridDim.x);
+    const int per = is_q ? io.q_per : io.kv_per;
+    const long long t0 = (long long)(is_q ? (int)blockIdx.x - kv_at : kv_at) * per;
+    const int n = (int)min((long long)per, (long long)c.B * c.N - t0);
     griddep_wait();
-    if (threadIdx.x < n) {
-        const long long tok = t0 + threadIdx.x;
-        const int b = (int)(tok / c.N), i = (int)(tok - (long long)b * c.N);
-        const Seq s = load_seq(c, b);
-        int slot = -1, page = 0;
-        if (i < s.q) {
-            slot = s.kv - s.q + i;
-            if (slot < 0) {
-                set_status(c.status, kDevBadPage);
-                slot = -1;
-            } else {
-                page = c.table[(size_t)b * c.max_pages + slot / c.page_size];
+    // slots and table, while the first loads are on their way
+    auto begin = [&] {
+        if (threadIdx.x < n) {
+            const long long x = t0 + threadIdx.x;
+            const int b = (int)(x / c.N), i = (int)(x - (long long)b * c.N);
+            const Seq s = load_seq(c, b);
+            int slot = -1, page = 0;
+            if (i < s.q) {
+                slot = s.kv - s.q + i;
+                if (slot < 0) {
+                    set_status(c.status, kDevBadPage);
+                    slot = -1;
+                } else if (!is_q) {
+                    page = c.table[(size_t)b * c.max_pages + slot / c.page_size];
+                }
             }
+            s_slot[threadIdx.x] = slot;
+            s_page[threadIdx.x] = page;
         }
-        s_slot[threadIdx.x] = slot;
-        s_page[threadIdx.x] = page;
+        __syncthreads();
+        if (p.on) {
+            rope_fill(p, table, n, 1.f, [&](int i) { return io.pos ? io.pos[t0 + i] : s_slot[i]; });
+            __syncthreads();
+        }
+    };
+    if (is_q) {
+        rope_rows<T, D, kRowBatch>(
+            p, table, reinterpret_cast<const T *>(io.q) + t0 * io.qs, io.qs,
+            reinterpret_cast<T *>(io.q_out) + t0 * io.H * D, (long long)io.H * D, n, io.H, begin,
+            [&](int t) { return s_slot[t] >= 0; });
+        return;
     }
-    __syncthreads();
-    if (p.on) rope_fill(p, table, n, 1.f, [&](int i) { return io.pos ? io.pos[t0 + i] : s_slot[i]; });
-
-    // keys and values: the rows of the next pass are loaded before this one's are stored
+    const int l = threadIdx.x % L, row0 = (threadIdx.x & 31) / L * L, rows = 2 * c.H_kv;
     bool bad = false;
     int tok = 0, h = threadIdx.x / L;
     auto wrap = [&](int &t, int &hh) {
@@ -202,76 +222,87 @@ __global__ void __launch_bounds__(kTokThreads, 4)
             ++t;
         }
     };
-    auto load = [&](int t, int hh, Raw8<T> &raw) {
-        if (t >= n || s_slot[t] < 0) return;
-        const T *src = hh < c.H_kv ? reinterpret_cast<const T *>(io.k) + (t0 + t) * io.ks + hh * D
-                                   : reinterpret_cast<const T *>(io.v) + (t0 + t) * io.vs + (hh - c.H_kv) * D;
-        raw.load(src + 8 * j);
+    auto load = [&](int t, int hh, Raw8<T> *raw) {
+        if (t >= n) return;
+        const T *src = (hh < c.H_kv ? reinterpret_cast<const T *>(io.k) + (t0 + t) * io.ks + hh * D
+                                    : reinterpret_cast<const T *>(io.v) + (t0 + t) * io.vs + (hh - c.H_kv) * D) +
+                       16 * l;
+        raw[0].load(src);
+        raw[1].load(src + 8);
     };
     wrap(tok, h);
-    Raw8<T> raw, next;
+    Raw8<T> raw[2];
     load(tok, h, raw);
-    if (p.on) __syncthreads();
-    const int hc = p.rot / 16;   // chunks of a half
+    begin();
+    const int hc = p.rot / 16;                    // chunks of 8 channels in a half
     for (int base = 0; base < n * rows; base += R) {   // CTA-uniform
-        int t2 = tok, h2 = h + R;
-        wrap(t2, h2);
-        load(t2, h2, next);
         const int slot = tok < n ? s_slot[tok] : -1;
         const bool is_k = slot >= 0 && h < c.H_kv, ok = slot >= 0;
-        float x[8];
-        raw.widen(x);
+        float x[16];
+        raw[0].widen(x);
+        raw[1].widen(x + 8);
+        const int tok1 = tok, h1 = h;
+        h += R;
+        wrap(tok, h);
+        if (base + R < n * rows) load(tok, h, raw);
         if (p.on && __any_sync(0xffffffffu, is_k)) {
-            const float *tc = table.c + (ok ? tok : 0) * kRopeMaxPairs, *ts = table.s + (ok ? tok : 0) * kRopeMaxPairs;
+            const float *tc = table.c + (ok ? tok1 : 0) * kRopeMaxPairs, *ts = table.s + (ok ? tok1 : 0) * kRopeMaxPairs;
             if (p.interleaved) {
-                if (is_k && 8 * j < p.rot) {
+                if (is_k && 16 * l < p.rot) rope_apply(p, table, tok1, l, x, x + 8);
+            } else {   // a chunk's partner is in another lane, in the other of its two chunks when hc is odd
+                const bool swap = hc & 1;
+                float o[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float u = x[2 * e], v = x[2 * e + 1], cc = tc[4 * j + e], ss = ts[4 * j + e];
-                        x[2 * e] = fmaf(u, cc, -v * ss);
-                        x[2 * e + 1] = fmaf(v, cc, u * ss);
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const int ch = 2 * l + k, pc = ch >= 2 * hc ? ch : ch < hc ? ch + hc : ch - hc;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[8 * k + e] = __shfl_sync(0xffffffffu, swap ? x[8 * (1 - k) + e] : x[8 * k + e], row0 + (pc >> 1));
                 }
-            } else {   // the partner chunk is another lane's
-                const bool first = j < hc, active = is_k && 8 * j < p.rot;
-                const int partner = row0 + (8 * j >= p.rot ? j : first ? j + hc : j - hc);
-                tc += 8 * (first ? j : j - hc);
-                ts += 8 * (first ? j : j - hc);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float o = __shfl_sync(0xffffffffu, x[e], partner);
-                    if (active) x[e] = fmaf(x[e], tc[e], first ? -o * ts[e] : o * ts[e]);
+                for (int k = 0; k < 2; ++k) {
+                    const int ch = 2 * l + k;
+                    const bool first = ch < hc;
+                    if (is_k && ch < 2 * hc) {
+                        const int at = 8 * (first ? ch : ch - hc);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const float4 cc = *reinterpret_cast<const float4 *>(tc + at + e);
+                            const float4 ss = *reinterpret_cast<const float4 *>(ts + at + e);
+                            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float q = o[8 * k + e + i] * sv[i];
+                                x[8 * k + e + i] = fmaf(x[8 * k + e + i], cv[i], first ? -q : q);
+                            }
+                        }
+                    }
                 }
             }
         }
         __nv_bfloat16 scale, low;
         bool nf = false;
-        const uint32_t code = quantise8(x, scale, low, nf);
-        if (ok) {
-            bad |= nf;
-            const int t = slot & 15;
-            uint8_t *blk = block_at<D>(c, s_page[tok], is_k ? h : h - c.H_kv, slot);
-            if (blk && is_k) {
-                *reinterpret_cast<uint32_t *>(blk + B::k_codes(t) + 4 * j) = code;
-                if (j % 4 == 0) *reinterpret_cast<__nv_bfloat162 *>(blk + B::k_pair(t, j / 4)) = __nv_bfloat162(scale, low);
-            } else if (blk) {
-                *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 64 * j / D) + (D == 128 ? (j & 1) * 4 : 0)) = code;
-                if (j % 4 == 0) {
-                    *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4)) = scale;
-                    *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, j / 4) + 4) = low;
-                }
+        const uint2 code = quantise16(x, scale, low, nf);
+        if (!ok) continue;
+        bad |= nf;
+        const int t = slot & 15;
+        uint8_t *blk = block_at<D>(c, s_page[tok1], is_k ? h1 : h1 - c.H_kv, slot);
+        if (!blk) continue;
+        if (is_k) {
+            *reinterpret_cast<uint2 *>(blk + B::k_codes(t) + 8 * l) = code;
+            if (l % 2 == 0) *reinterpret_cast<__nv_bfloat162 *>(blk + B::k_pair(t, l / 2)) = __nv_bfloat162(scale, low);
+        } else {
+            if constexpr (D == 128) {
+                *reinterpret_cast<uint2 *>(blk + B::v_codes(t, l)) = code;
+            } else {
+                *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 2 * l)) = code.x;
+                *reinterpret_cast<uint32_t *>(blk + B::v_codes(t, 2 * l + 1)) = code.y;
             }
+            // the pair's two lanes write one number each
+            *reinterpret_cast<__nv_bfloat16 *>(blk + B::v_scale(t, l / 2) + 4 * (l & 1)) = l & 1 ? low : scale;
         }
-        raw = next;
-        tok = t2;
-        h = h2;
     }
     if (bad) set_status(c.status, kDevNonFinite);
-    if (io.H > 0)
-        rope_rows<T, D>(
-            p, table, reinterpret_cast<const T *>(io.q) + t0 * io.qs, io.qs,
-            reinterpret_cast<T *>(io.q_out) + t0 * io.H * D, (long long)io.H * D, n, io.H, [] {},
-            [&](int t) { return s_slot[t] >= 0; });
 }
 
 // 32 bytes of an output row: one store when the tensors allow it (wide: 32-byte aligned).

@@ -112,8 +112,11 @@ __device__ __forceinline__ void rope_fill(const RopeParams &p, RopeTable &t, int
     const int pairs = p.rot / 2;   // 8 .. 64
     for (int i = threadIdx.x; i < n * pairs; i += kTokThreads) {
         const int tok = i / pairs, e = i - tok * pairs;
+        // a load through the generic address: as constant-bank reads the lanes' different addresses would take turns
+        double turns;
+        asm("ld.f64 %0, [%1];" : "=d"(turns) : "l"(p.turns + e));
         float c, s;
-        turn(pos(tok), p.turns[e], p.amp, c, s);
+        turn(pos(tok), turns, p.amp, c, s);
         t.c[tok * kRopeMaxPairs + e] = c;
         t.s[tok * kRopeMaxPairs + e] = sign * s;
     }
@@ -163,13 +166,13 @@ __device__ __forceinline__ void rope_apply(const RopeParams &p, const RopeTable 
     }
 }
 
-// Rows (token, head) of n tokens from x to y, kRowBatch passes of loads at a
-// time (kept as stored: widened they would halve the rows in flight).  begin()
-// runs once, between the first loads and the first use of the table; a token
-// is skipped where use(token) is false.
+// Rows (token, head) of n tokens from x to y, Batch passes of loads at a time
+// (kept as stored: widened they would halve the rows in flight).  begin() runs
+// once, after the first loads have been started, and fills the table; a token's
+// rows are not written where use(token) is false.
 constexpr int kRowBatch = 2;
 
-template <typename T, int D, typename Begin, typename Use>
+template <typename T, int D, int Batch, typename Begin, typename Use>
 __device__ __forceinline__ void rope_rows(const RopeParams &p, const RopeTable &table, const T *x, long long xs, T *y,
                                           long long ys, int n, int H, Begin &&begin, Use &&use)
 {
@@ -186,12 +189,12 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, const RopeTable &
     };
     wrap(tok, h);
     bool started = false;
-    for (int base = 0; base < n * H; base += kRowBatch * R) {   // CTA-uniform
-        Raw8<T> ra[kRowBatch], rb[kRowBatch];
+    for (int base = 0; base < n * H; base += Batch * R) {   // CTA-uniform
+        Raw8<T> ra[Batch], rb[Batch];
         int t2 = tok, h2 = h;
 #pragma unroll
-        for (int k = 0; k < kRowBatch; ++k) {
-            if (t2 < n && use(t2)) {
+        for (int k = 0; k < Batch; ++k) {
+            if (t2 < n) {
                 const T *src = x + t2 * xs + h2 * D;
                 ra[k].load(src + 8 * ca);
                 rb[k].load(src + 8 * cb);
@@ -204,7 +207,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams &p, const RopeTable &
             started = true;
         }
 #pragma unroll
-        for (int k = 0; k < kRowBatch; ++k) {
+        for (int k = 0; k < Batch; ++k) {
             if (tok < n && use(tok)) {
                 float a[8], b[8];
                 ra[k].widen(a);
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kTokThreads, 4) rope_kernel(const __grid_const
     const long long t0 = (long long)blockIdx.x * io.per_cta;
     const int n = (int)min((long long)io.per_cta, io.tokens - t0);
     griddep_wait();
-    rope_rows<T, D>(
+    rope_rows<T, D, kRowBatch>(
         p, table, reinterpret_cast<const T *>(io.x) + t0 * io.xs, io.xs, reinterpret_cast<T *>(io.y) + t0 * io.ys, io.ys, n,
         io.H,
         [&] {

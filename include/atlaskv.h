@@ -438,8 +438,8 @@ typedef struct {
     const int32_t *block_table;  /* [B][max_pages] page ids; columns past a sequence's length are not read */
     const int32_t *kv_len;     /* [B] tokens of the sequence, the new ones among them */
     const int32_t *q_len;      /* [B] new tokens, 0 .. N, or NULL: N each.  Row n < q_len[b] of a token tensor is
-                                  slot kv_len[b] - q_len[b] + n; rows n >= q_len[b] are padding: not read, and
-                                  left as they are in outputs */
+                                  slot kv_len[b] - q_len[b] + n; rows n >= q_len[b] are padding: their values do
+                                  not matter, and they are left as they are in outputs */
 } atlaskv_seqs;
 
 /* Bytes of one page (host only). */
