@@ -41,11 +41,10 @@ __device__ __forceinline__ void ca_write(const CacheParams &c, const CacheAttend
 // n G + g; a unit of work is 32 stored tokens against a block of 8 NT rows.
 // Per row the online softmax keeps a running maximum m, sum l and output O:
 //     S = q k;  p = 2^(S scale log2 e - m);  l += sum p;  O += p v.
-// What bounds it: the codes are read once and every code becomes a bfloat16
-// (an AND-OR into the mantissa of 128, minus 128, one fused multiply-add with
-// the group's scale and minimum: exactly the stored number), about 0.8
-// instructions a code against 0.625 bytes, so HBM and the issue slots are both
-// near their limits.
+// What bounds it: the codes are read once and every code becomes a bfloat16,
+// exactly the stored number, at 1.6 instructions a pair; with the softmax and
+// the products that is about 0.07 warp instructions a code against 0.625 bytes, so the
+// issue slots are nearer their limit than HBM.
 //
 // The products run on m16n8k16 with the cache as the 16-row operand, S^T = K
 // Q^T and O^T = V^T P^T: a decode step has few rows, so they take the 8-wide
@@ -248,37 +247,47 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
         const int mine_n = cnt > warp ? (cnt - warp + kCaWarps - 1) / kCaWarps : 0;
         const int32_t *tab = c.table + (size_t)b * c.max_pages;
         const int pshift = 31 - __clz(c.page_size);
-        auto page_of = [&](int i, int blk) -> int {   // page of block blk of this warp's unit i
-            const int slot = (k0 + warp + kCaWarps * i) * kCaUnit + 16 * blk;
-            return i < mine_n && slot < s.kv ? tab[slot >> pshift] : 0;
+        // lane j looks the blocks of this warp's units j, j + 32, .. up in the table: block indices in the pool
+        auto find = [&](int i, uint32_t &x, uint32_t &y) {
+            const int slot = (k0 + warp + kCaWarps * i) * kCaUnit;
+            x = y = 0u;
+            if (i >= mine_n || slot >= s.kv) return;
+            auto at = [&](int sl) -> uint32_t {
+                int page = tab[sl >> pshift];
+                if ((unsigned)page >= (unsigned long long)c.n_pages) {   // reported; another page's bytes stand in
+                    set_status(c.status, kDevBadPage);
+                    page = 0;
+                }
+                return (uint32_t)((((long long)page * c.H_kv + hkv) << (pshift - 4)) + ((sl & (c.page_size - 1)) >> 4));
+            };
+            x = at(slot);
+            y = slot + 16 >= s.kv ? 0u : c.page_size > 16 ? x + 1 : at(slot + 16);
         };
-        int pg0 = page_of(lane, 0), pg1 = page_of(lane, 1), nx0 = 0, nx1 = 0;
-        if (mine_n > 32) {
-            nx0 = page_of(32 + lane, 0);
-            nx1 = page_of(32 + lane, 1);
-        }
+        uint32_t at0, at1, nx0 = 0, nx1 = 0;
+        find(lane, at0, at1);
+        if (mine_n > 32) find(32 + lane, nx0, nx1);
         auto issue = [&](int i) {   // warp-uniform i
             const int j = i & 31;
             if (j == 0 && i > 0) {
-                pg0 = nx0;
-                pg1 = nx1;
-                nx0 = page_of(i + 32 + lane, 0);
-                nx1 = page_of(i + 32 + lane, 1);
+                at0 = nx0;
+                at1 = nx1;
+                find(i + 32 + lane, nx0, nx1);
             }
-            const int a = __shfl_sync(0xffffffffu, pg0, j), d = __shfl_sync(0xffffffffu, pg1, j);
+            const uint32_t x = __shfl_sync(0xffffffffu, at0, j), y = __shfl_sync(0xffffffffu, at1, j);
             if (lane == 0) {
-                const int key = (k0 + warp + kCaWarps * i) * kCaUnit, st = (T_ + i) % S;
-                const bool two = key + 16 < s.kv;
+                const int st = (T_ + i) % S;
                 const uint32_t bar = bars + 8 * st, dst = ring + st * C::kUnitBytes;
-                const uint8_t *p0 = block_at<D>(c, a, hkv, key), *p1 = two ? block_at<D>(c, d, hkv, key + 16) : p0;
-                if (!p0) p0 = c.pages;   // reported; any page's bytes stand in
-                if (!p1) p1 = c.pages;
-                tc::mbar_arrive_expect_tx(bar, two ? 2 * B::kBytes : B::kBytes);
-                if (two && p1 == p0 + B::kBytes) {
-                    bulk_load(dst, p0, 2 * B::kBytes, bar);
+                const uint8_t *src = c.pages + (unsigned long long)x * B::kBytes;
+                if (y == x + 1) {
+                    tc::mbar_arrive_expect_tx(bar, 2 * B::kBytes);
+                    bulk_load(dst, src, 2 * B::kBytes, bar);
+                } else if ((k0 + warp + kCaWarps * i) * kCaUnit + 16 < s.kv) {
+                    tc::mbar_arrive_expect_tx(bar, 2 * B::kBytes);
+                    bulk_load(dst, src, B::kBytes, bar);
+                    bulk_load(dst + B::kBytes, c.pages + (unsigned long long)y * B::kBytes, B::kBytes, bar);
                 } else {
-                    bulk_load(dst, p0, B::kBytes, bar);
-                    if (two) bulk_load(dst + B::kBytes, p1, B::kBytes, bar);
+                    tc::mbar_arrive_expect_tx(bar, B::kBytes);
+                    bulk_load(dst, src, B::kBytes, bar);
                 }
             }
         };
@@ -361,7 +370,8 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
             for (int k = 0; k < 2; ++k) {
                 if (k == 1 && !two) break;
                 const uint8_t *blk = ub + k * B::kBytes;
-                uint32_t w[2][D / 32], s2[2], m2[2];
+                uint32_t w[2][D / 32];
+                Scale2 s2[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if constexpr (D == 128) {
@@ -377,18 +387,16 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                     }
                     const uint32_t pr =
                         *reinterpret_cast<const uint32_t *>(blk + B::k_pair(r + 8 * h, t * (D / 4) / 32));
-                    s2[h] = prmt(pr, pr, 0x1010);
-                    m2[h] = prmt(pr, pr, 0x3232);
+                    s2[h] = scale2(prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232));
                 }
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x)
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t n0[4], n1[4];
+                    stored8(w[0][x], s2[0], n0);
+                    stored8(w[1][x], s2[1], n1);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {   // contraction step 2 x + y
-                        uint32_t a[4];
-                        a[0] = stored2(w[0][x] >> (8 * y), s2[0], m2[0]);
-                        a[1] = stored2(w[1][x] >> (8 * y), s2[1], m2[1]);
-                        a[2] = stored2(w[0][x] >> (8 * y + 4), s2[0], m2[0]);
-                        a[3] = stored2(w[1][x] >> (8 * y + 4), s2[1], m2[1]);
+                        const uint32_t a[4] = {n0[2 * y], n1[2 * y], n0[2 * y + 1], n1[2 * y + 1]};
 #pragma unroll
                         for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -402,6 +410,7 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                                 }
                             }
                     }
+                }
             }
 
             // ---- softmax: element (token r + 8 (e / 2), row 2 t + (e & 1)) ----
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[k][e] = sc[k][j][e] * io.scale_log2;
+                    for (int e = 0; e < 4; ++e) v[k][e] = sc[k][j][e];
                 if (edge) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
@@ -421,8 +430,8 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                         for (int e = 0; e < 4; ++e)
                             if (key0 + 16 * k + r + 8 * (e >> 1) > lim[j][e & 1]) v[k][e] = -INFINITY;
                 }
-                float x0 = fmaxf(fmaxf(v[0][0], v[0][2]), fmaxf(v[1][0], v[1][2]));
-                float x1 = fmaxf(fmaxf(v[0][1], v[0][3]), fmaxf(v[1][1], v[1][3]));
+                float x0 = fmaxf(max3(v[0][0], v[0][2], v[1][0]), v[1][2]) * io.scale_log2;
+                float x1 = fmaxf(max3(v[0][1], v[0][3], v[1][1]), v[1][3]) * io.scale_log2;
                 // the maximum moves only when a logit exceeds it by 2^8: any m gives the same quotient O / l
                 if (__any_sync(0xffffffffu, x0 > m[j][0] + 8.f || x1 > m[j][1] + 8.f)) {
 #pragma unroll
@@ -445,11 +454,11 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                         acc[j][d][3] *= f1;
                     }
                 }
-                const float z0 = m[j][0] == -INFINITY ? 0.f : m[j][0], z1 = m[j][1] == -INFINITY ? 0.f : m[j][1];
+                const float z0 = m[j][0] == -INFINITY ? 0.f : -m[j][0], z1 = m[j][1] == -INFINITY ? 0.f : -m[j][1];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[k][e] = tc::fast_exp2(v[k][e] - ((e & 1) ? z1 : z0));
+                    for (int e = 0; e < 4; ++e) v[k][e] = tc::fast_exp2(fmaf(v[k][e], io.scale_log2, (e & 1) ? z1 : z0));
                     l[j][0] += v[k][0] + v[k][2];
                     l[j][1] += v[k][1] + v[k][3];
 #pragma unroll
@@ -472,7 +481,8 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
             for (int k = 0; k < 2; ++k) {
                 if (k == 1 && !two) break;
                 const uint8_t *blk = ub + k * B::kBytes;
-                uint32_t x[2][D / 32], s2[2], m2[2];   // 4 channels of a token pair each
+                uint32_t x[2][D / 32];   // 4 channels of a token pair each
+                Scale2 s2[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if constexpr (D == 128) {
@@ -488,27 +498,27 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                     }
                     const uint2 pr = *reinterpret_cast<const uint2 *>(
                         blk + B::kVS + ((h * B::kGroups + r * (D / 8) / 32) * 4 + t) * 8);
-                    s2[h] = pr.x;
-                    m2[h] = pr.y;
+                    uint32_t keep = 0xffffffffu;
                     if (edge) {   // tokens past the sequence may hold anything, NaN too
                         const int a = key0 + 16 * k + 8 * h + 2 * t;
-                        const uint32_t keep = (a < s.kv ? 0xffffu : 0u) | (a + 1 < s.kv ? 0xffff0000u : 0u);
-                        s2[h] &= keep;
-                        m2[h] &= keep;
+                        keep = (a < s.kv ? 0xffffu : 0u) | (a + 1 < s.kv ? 0xffff0000u : 0u);
                     }
+                    s2[h] = scale2(pr.x & keep, pr.y & keep);
                 }
 #pragma unroll
-                for (int d = 0; d < KS; ++d) {   // channels 2 d, 2 d + 1 of the slice
-                    uint32_t a[4];
-                    const int y = d >> 1, sh = 8 * (d & 1);
-                    a[0] = stored2(x[0][y] >> sh, s2[0], m2[0]);
-                    a[1] = stored2(x[0][y] >> (sh + 4), s2[0], m2[0]);
-                    a[2] = stored2(x[1][y] >> sh, s2[1], m2[1]);
-                    a[3] = stored2(x[1][y] >> (sh + 4), s2[1], m2[1]);
+                for (int y = 0; y < D / 32; ++y) {   // channels 4 y .. 4 y + 3 of the slice
+                    uint32_t n0[4], n1[4];
+                    stored8(x[0][y], s2[0], n0);
+                    stored8(x[1][y], s2[1], n1);
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
+                    for (int e = 0; e < 2; ++e) {    // channels 2 d, 2 d + 1
+                        const int d = 2 * y + e;
+                        const uint32_t a[4] = {n0[2 * e], n0[2 * e + 1], n1[2 * e], n1[2 * e + 1]};
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) mma16816(acc[j][d], a, pf[p][j][k]);
+                        for (int p = 0; p < P; ++p)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) mma16816(acc[j][d], a, pf[p][j][k]);
+                    }
                 }
             }
             __syncwarp();   // the stage may be refilled

@@ -511,16 +511,14 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                 if (failed) break;
                 const bool tail = key0 + kKeys > g.e.s.kv;   // tokens past the sequence become zeros
                 // 32 channels (group gr of the row) of token `key` of half h: 4 chunks of 16 bytes
-                auto put = [&](uint8_t *tile, int h, int gr, const uint32_t *w, uint32_t s2, uint32_t m2) {
+                auto put = [&](uint8_t *tile, int h, int gr, const uint32_t *w, const Scale2 &s) {
                     const bool zero = tail && key0 + h * kHalf + key >= g.e.s.kv;
                     uint8_t *dst = tile + (gr >> 1) * (kKeys * 128) + (h * kHalf + key) * 128;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint4 v;
-                        v.x = stored2(w[i], s2, m2);
-                        v.y = stored2(w[i] >> 4, s2, m2);
-                        v.z = stored2(w[i] >> 8, s2, m2);
-                        v.w = stored2(w[i] >> 12, s2, m2);
+                        uint32_t o[4];
+                        stored8(w[i], s, o);
+                        uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
                         if (zero) v = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4 *>(dst + ((((gr & 1) * 4 + i) ^ (key & 7)) << 4)) = v;
                     }
@@ -535,7 +533,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                         const uint32_t pr = *reinterpret_cast<const uint32_t *>(blk + B::k_pair(tok, gr));
                         const uint4 a = *reinterpret_cast<const uint4 *>(blk + B::k_codes(tok) + gr * 16);
                         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-                        put(ctc_smem + SM::kOffK + st * SM::kT, h, gr, w, prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232));
+                        put(ctc_smem + SM::kOffK + st * SM::kT, h, gr, w, scale2(prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232)));
                     }
                 }
                 fence_async_smem();
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                             for (int i = 0; i < 4; ++i)
                                 w[i] = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(tok, 4 * gr + i));
                         }
-                        put(ctc_smem + SM::kOffV + st * SM::kT, h, gr, w, s1 | s1 << 16, m1 | m1 << 16);
+                        put(ctc_smem + SM::kOffV + st * SM::kT, h, gr, w, scale2(s1 | s1 << 16, m1 | m1 << 16));
                     }
                 }
                 fence_async_smem();

@@ -140,14 +140,43 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
     return make_uint2(w[0] - 0x4b400000u * 0x11111111u, w[1] - 0x4b400000u * 0x11111111u);
 }
 
-// Two codes at bits 0..3 and 16..19 -> bf16x2 of the stored numbers.
-__device__ __forceinline__ uint32_t stored2(uint32_t x, uint32_t scale2, uint32_t low2)
+// Codes to numbers, two at a time (bfloat16 pairs).  A nibble alone in the low 8
+// bits of a 16-bit lane is the tiny bfloat16 c 2^-133 (bits 0..3) or c 2^-129
+// (bits 4..7: the exponent's last bit continues the subnormals linearly).  Times
+// 2^127 it is c 2^-6 or c 2^-2, exactly, and one fused multiply-add with the scale
+// times 2^6 or 2^2 (at most 2^123) and the minimum rounds m + c s once.  So a
+// word of 8 codes needs one shift, 4 ANDs, 4 products and 4 fused operations.
+struct Scale2 {
+    uint32_t lo, hi, low;   // scale 2^6, scale 2^2, minimum
+};
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
-    uint32_t c, r;
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(c) : "r"(x));   // (x & mask) | 128.0
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c), "r"(0x43004300u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(scale2), "r"(low2));
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+__device__ __forceinline__ Scale2 scale2(uint32_t s2, uint32_t m2)
+{
+    return {mul_bf16x2(s2, 0x42804280u), mul_bf16x2(s2, 0x40804080u), m2};
+}
+
+__device__ __forceinline__ uint32_t stored2(uint32_t masked, uint32_t scale, uint32_t low)
+{
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(mul_bf16x2(masked, 0x7f007f00u)), "r"(scale), "r"(low));
+    return r;
+}
+
+// Pairs (nibble i, nibble i + 4) of a word, i = 0 .. 3.
+__device__ __forceinline__ void stored8(uint32_t w, const Scale2 &s, uint32_t *out)
+{
+    const uint32_t v = w >> 8;
+    out[0] = stored2(w & 0x000f000fu, s.lo, s.low);
+    out[1] = stored2(w & 0x00f000f0u, s.hi, s.low);
+    out[2] = stored2(v & 0x000f000fu, s.lo, s.low);
+    out[3] = stored2(v & 0x00f000f0u, s.hi, s.low);
 }
 
 struct AppendIo {
@@ -319,11 +348,10 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide)
 }
 
 // bf16 pairs (channel 2 i, 2 i + 1) of the 8 codes of a word.
-__device__ __forceinline__ void stored8(uint32_t w, uint32_t scale2, uint32_t low2, uint32_t *out)
+__device__ __forceinline__ void stored8_in_order(uint32_t w, const Scale2 &s, uint32_t *out)
 {
-    uint32_t v[4];   // channels (i, i + 4)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = stored2(w >> (4 * i), scale2, low2);
+    uint32_t v[4];
+    stored8(w, s, v);
     out[0] = __byte_perm(v[0], v[1], 0x5410);
     out[1] = __byte_perm(v[2], v[3], 0x5410);
     out[2] = __byte_perm(v[0], v[1], 0x7632);
@@ -402,15 +430,15 @@ __global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Cache
         const size_t at = (((size_t)b * c.N + slot - first) * c.H_kv + h) * D + 16 * j;
         uint32_t out[8];
         if (k_out) {
-            const uint32_t s2 = __byte_perm(kp[k], kp[k], 0x1010), m2 = __byte_perm(kp[k], kp[k], 0x3232);
-            stored8(kc[k].x, s2, m2, out);
-            stored8(kc[k].y, s2, m2, out + 4);
+            const Scale2 s2 = scale2(__byte_perm(kp[k], kp[k], 0x1010), __byte_perm(kp[k], kp[k], 0x3232));
+            stored8_in_order(kc[k].x, s2, out);
+            stored8_in_order(kc[k].y, s2, out + 4);
             store16<T>(k_out + at, out, wide);
         }
         if (v_out) {
-            const uint32_t s2 = vs[k] | vs[k] << 16, m2 = vm[k] | vm[k] << 16;
-            stored8(vc[k].x, s2, m2, out);
-            stored8(vc[k].y, s2, m2, out + 4);
+            const Scale2 s2 = scale2(vs[k] | vs[k] << 16, vm[k] | vm[k] << 16);
+            stored8_in_order(vc[k].x, s2, out);
+            stored8_in_order(vc[k].y, s2, out + 4);
             store16<T>(v_out + at, out, wide);
         }
     }
