@@ -185,8 +185,12 @@ atlaskv_status cache_params(const atlaskv_cache *c, const atlaskv_seqs *s, akv::
 }
 
 // Row blocks of 8, 16 or 32 rows: the fewest that hold a KV head's rows (a
-// unit's codes are turned into bfloat16 once per row block).
-int row_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// unit's codes are turned into bfloat16 once per row block).  float32 queries
+// are three bfloat16 parts: 16 rows at most, 32 would not fit the registers.
+int row_tiles(int dtype, long long rows) { return rows <= 8 ? 1 : rows <= 16 || dtype == ATLASKV_F32 ? 2 : 4; }
+
+// Slots that the block table can name, an upper bound of every length.
+long long slots_of(const akv::CacheParams &p) { return (long long)p.max_pages * p.page_size; }
 
 template <typename T, int D, int NT>
 int ca_ctas(const atlaskv_cache *c)
@@ -208,9 +212,10 @@ atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, cons
     AKV_RET(akv_smem_limit(reinterpret_cast<const void *>(akv::cache_attend_kernel<T, D, NT>), C::kSmem));
     const int n = ca_ctas<T, D, NT>(c);
     AKV_RET(launch_pdl(akv::cache_attend_kernel<T, D, NT>, dim3(n), akv::kCaThreads, C::kSmem, s, p, a));
-    if (n == 1) return ATLASKV_OK;   // no cuts
-    return launch_pdl(akv::cache_combine_kernel<T, D, C::kRB, 4>, dim3(n - 1, C::kRB / 2), akv::kJoinThreads, 0, s, p, a,
-                      n);
+    // no cuts whatever the lengths are: no join
+    const long long items = (long long)p.B * p.H_kv * (((long long)p.N * a.G + C::kRB - 1) / C::kRB);
+    if (akv::ca_whole(items, n, slots_of(p) / akv::kCaUnit + 1, 0, akv::kCaPartialUnits)) return ATLASKV_OK;
+    return launch_pdl(akv::cache_combine_kernel<T, D, C::kRB>, dim3(n - 1, 8), akv::kJoinThreads, 0, s, p, a, n);
 }
 
 // Many rows of bfloat16 queries: tcgen05 (the few-rows kernel would turn the
@@ -233,18 +238,15 @@ atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, cons
     const int n = c->num_sms;
     AKV_RET(launch_pdl(akv::cache_attend_tc_kernel<D>, dim3(n), akv::ctc::kThreads, akv::ctc::Smem<D>::kBytes, s, p, a,
                        (int)nb));
-    if (n == 1) return ATLASKV_OK;
-    return launch_pdl(akv::cache_combine_kernel<__nv_bfloat16, D, RB, 1>, dim3(n - 1, RB / 8), akv::kJoinThreads, 0, s,
-                      p, a, n);
+    if (akv::ca_whole(nb * p.B * p.H_kv, n, slots_of(p) / akv::ctc::kKeys + 1, 0, akv::ctc::kPartialUnits)) return ATLASKV_OK;
+    return launch_pdl(akv::cache_combine_kernel<__nv_bfloat16, D, RB>, dim3(n - 1, 32), akv::kJoinThreads, 0, s, p, a, n);
 }
 
 // f<T, D, NT>(args...) for the call's type, head dimension and rows
 #define AKV_CA(dtype, D, NT, f, ...)                                                                              \
     ((dtype) == ATLASKV_F32                                                                                       \
-         ? ((D) == 64 ? ((NT) == 1 ? f<float, 64, 1>(__VA_ARGS__) : (NT) == 2 ? f<float, 64, 2>(__VA_ARGS__)      \
-                                                                              : f<float, 64, 4>(__VA_ARGS__))     \
-                      : ((NT) == 1 ? f<float, 128, 1>(__VA_ARGS__) : (NT) == 2 ? f<float, 128, 2>(__VA_ARGS__)    \
-                                                                               : f<float, 128, 4>(__VA_ARGS__)))  \
+         ? ((D) == 64 ? ((NT) == 1 ? f<float, 64, 1>(__VA_ARGS__) : f<float, 64, 2>(__VA_ARGS__))                 \
+                      : ((NT) == 1 ? f<float, 128, 1>(__VA_ARGS__) : f<float, 128, 2>(__VA_ARGS__)))              \
          : ((D) == 64 ? ((NT) == 1   ? f<__nv_bfloat16, 64, 1>(__VA_ARGS__)                                       \
                          : (NT) == 2 ? f<__nv_bfloat16, 64, 2>(__VA_ARGS__)                                       \
                                      : f<__nv_bfloat16, 64, 4>(__VA_ARGS__))                                      \
@@ -482,7 +484,7 @@ atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *c, int32_t dtyp
     if (B == 0) return ATLASKV_OK;
     const long long rows = (long long)N * (H / c->d.n_kv_heads);
     if (use_tc(dtype, rows)) *bytes = c->d.head_dim == 64 ? tc_workspace<64>(c) : tc_workspace<128>(c);
-    else *bytes = AKV_CA(dtype, c->d.head_dim, row_tiles(rows), ca_workspace, c);
+    else *bytes = AKV_CA(dtype, c->d.head_dim, row_tiles(dtype, rows), ca_workspace, c);
     return ATLASKV_OK;
 }
 
@@ -519,7 +521,7 @@ atlaskv_status atlaskv_cache_attend(atlaskv_cache *c, const atlaskv_seqs *seqs, 
     if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (use_tc(io->dtype, rows)) return D == 64 ? launch_tc<64>(c, p, a, s) : launch_tc<128>(c, p, a, s);
-    return AKV_CA(io->dtype, D, row_tiles(rows), launch_ca, c, p, a, s);
+    return AKV_CA(io->dtype, D, row_tiles(io->dtype, rows), launch_ca, c, p, a, s);
 }
 
 }  // extern "C"

@@ -85,12 +85,36 @@ struct Ca {
     static constexpr int kSlot = kRB * (D + 2);             // floats of a partial: O, m, l
 };
 
+// A divided item costs about as much as this many units more on every CTA (the
+// partials, a second launch's work: about 4 us against 0.1 us a unit of a CTA).
+constexpr int kCaPartialUnits = 40;
+
+// Whether whole items, round-robin over the CTAs, end about as early as equal
+// runs of units would.
+__host__ __device__ __forceinline__ bool ca_whole(long long items, long long ctas, long long longest, long long total,
+                                                  int partial_units)
+{
+    return (items + ctas - 1) / ctas * longest <= (total + ctas - 1) / ctas + partial_units;
+}
+
 // What CTA c left for the join: its first item, where in it the CTA began.
 struct CaDesc {
     long long total;        // units of the call
     int active;             // CTAs with units
     int k0, units;          // first unit within the item (0: not divided before it); the item's units
     int b, hkv, rb;
+};
+
+// A CTA's walk over its runs of units, kept in shared memory by one thread.
+struct CaWalk {
+    long long total, u, end, off;   // units of the call; next unit and the run's end; the next one's offset within b
+    int active, whole, b;           // CTAs with units; whole items (off counts items, u and end do not matter)?
+};
+
+// One stretch of an item's units.
+struct CaSeg {
+    Seq s;
+    int b, hkv, rb, k0, cnt, units;   // cnt = 0: no more
 };
 
 __device__ __forceinline__ long long ca_start(long long total, int active, int c) { return total * c / active; }
@@ -154,9 +178,10 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
     using B = Blk<D>;
     constexpr int P = C::kParts, KS = D / 16, S = C::kStages;
     extern __shared__ __align__(128) uint8_t ca_smem[];
-    __shared__ long long s_sum[kCaWarps];
-    __shared__ long long s_off;
-    __shared__ int s_b;
+    __shared__ long long s_sum[kCaWarps], s_items[kCaWarps];
+    __shared__ int s_top[kCaWarps];
+    __shared__ CaWalk walk;
+    __shared__ CaSeg segs[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
     const uint32_t sb = tc::smem_addr(ca_smem);
     const uint32_t ring = sb + warp * S * C::kUnitBytes, bars = sb + C::kOffBar + warp * S * 8;
@@ -176,62 +201,99 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
         return (long long)c.H_kv * n_blocks(s) * n_units(s);
     };
     const int per = (c.B + kCaThreads - 1) / kCaThreads, b_lo = min(c.B, tid * per), b_hi = min(c.B, b_lo + per);
-    long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += total_of(b);
+    long long mine = 0, items = 0;
+    int top = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const Seq s = load_seq(c, b);
+        const long long n = (long long)c.H_kv * n_blocks(s);
+        items += n;
+        mine += n * n_units(s);
+        top = max(top, n > 0 ? n_units(s) : 0);
+    }
     long long scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += v;
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
-    if (lane == 31) s_sum[warp] = scan;
+    if (lane == 31) {
+        s_sum[warp] = scan;
+        s_items[warp] = items;
+        s_top[warp] = top;
+    }
     __syncthreads();
-    long long total = 0, before = scan - mine;
+    long long total = 0, before = scan - mine, all = 0;
+    int longest = 0;
 #pragma unroll
     for (int w = 0; w < kCaWarps; ++w) {
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
+        all += s_items[w];
+        longest = max(longest, s_top[w]);
     }
-    const int cta = blockIdx.x;
-    const int active = (int)max(1LL, min((long long)gridDim.x, (total + kCaWarps - 1) / kCaWarps));
-    CaDesc *desc = reinterpret_cast<CaDesc *>(io.ws) + cta;
-    float *slots = reinterpret_cast<float *>(io.ws + gridDim.x * sizeof(CaDesc)) + (size_t)cta * 2 * C::kSlot;
-    if (cta >= active || total == 0) {   // CTA-uniform
-        if (tid == 0) desc->k0 = 0;
-        return;
-    }
-    long long u = ca_start(total, active, cta);
-    const long long u_end = ca_start(total, active, cta + 1);
-    if (u >= before && u < before + mine) {
-        long long off = u - before;
-        int b = b_lo;
-        for (;; ++b) {
-            const long long n = total_of(b);
-            if (off < n) break;
-            off -= n;
+    CaDesc *desc = reinterpret_cast<CaDesc *>(io.ws) + blockIdx.x;
+    if (tid == 0) desc->k0 = 0;   // until the CTA begins inside an item
+    {
+        const bool whole = ca_whole(all, gridDim.x, longest, total, kCaPartialUnits);
+        const int active = (int)max(1LL, min((long long)gridDim.x, (total + kCaWarps - 1) / kCaWarps));
+        if (blockIdx.x >= (whole ? all : min((long long)active, total))) return;   // CTA-uniform
+        const long long u = whole ? 0 : ca_start(total, active, blockIdx.x);
+        if (u >= before && u < before + mine) {   // the thread whose sequences hold the CTA's first unit
+            long long off = u - before;
+            int b = b_lo;
+            for (; !whole; ++b) {
+                const long long n = total_of(b);
+                if (off < n) break;
+                off -= n;
+            }
+            walk = CaWalk{total, u, ca_start(total, active, blockIdx.x + 1), whole ? blockIdx.x : off, active, whole,
+                          whole ? 0 : b};
         }
-        s_b = b;
-        s_off = off;
+    }
+    // the next stretch, by one thread: while the CTA is busy with the one before
+    auto advance = [&](CaSeg &g) {
+        CaWalk w = walk;
+        g.cnt = 0;
+        while (w.b < c.B && (w.whole || w.u < w.end)) {
+            const Seq s = load_seq(c, w.b);
+            const int nb = n_blocks(s), units = n_units(s);
+            const long long n = (long long)c.H_kv * nb * (w.whole ? 1 : units);
+            if (w.off >= n) {
+                w.off -= n;
+                ++w.b;
+                continue;
+            }
+            const int item = (int)(w.whole ? w.off : w.off / units);
+            g.s = s;
+            g.b = w.b;
+            g.hkv = item / nb;
+            g.rb = item - g.hkv * nb;
+            g.units = units;
+            g.k0 = w.whole ? 0 : (int)(w.off - (long long)item * units);
+            g.cnt = w.whole ? units : (int)min((long long)(units - g.k0), w.end - w.u);
+            w.u += g.cnt;
+            w.off += w.whole ? gridDim.x : g.cnt;
+            break;
+        }
+        walk = w;
+    };
+    __syncthreads();
+    if (tid == 0) {
+        advance(segs[0]);
+        if (segs[0].k0 > 0)
+            *desc = CaDesc{walk.total, walk.active, segs[0].k0, segs[0].units, segs[0].b, segs[0].hkv, segs[0].rb};
     }
     __syncthreads();
-    int b = s_b;
-    long long off = s_off;
 
     int T_ = 0;   // units this warp has taken from its ring
-    bool failed = false, first = true;
-    while (u < u_end) {
-        const Seq s = load_seq(c, b);
-        const int nb = n_blocks(s), units = n_units(s);
-        const long long n = (long long)c.H_kv * nb * units;
-        if (off >= n) {
-            off -= n;
-            ++b;
-            continue;
-        }
-        const int item = (int)(off / units), k0 = (int)(off - (long long)item * units);
-        const int hkv = item / nb, rb = item - hkv * nb;
-        const int cnt = (int)min((long long)(units - k0), u_end - u);
-        if (first && tid == 0) *desc = CaDesc{total, active, k0, units, b, hkv, rb};
+    bool failed = false;
+    for (int si = 0;; si ^= 1) {
+        const CaSeg &seg = segs[si];
+        if (seg.cnt == 0) break;   // CTA-uniform
+        const Seq s = seg.s;
+        const int b = seg.b, hkv = seg.hkv, rb = seg.rb, k0 = seg.k0, cnt = seg.cnt;
         const int R = io.G * s.q, row0 = rb * C::kRB;
         // last visible slot of this lane's rows (row 2 t, 2 t + 1 of each 8), and of the block's first row
         int lim[NT][2];
@@ -293,6 +355,7 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
         };
         const int n_run = s.kv > 0 && !failed ? mine_n : 0;
         for (int i = 0; i < min(S - 1, n_run); ++i) issue(i);
+        if (tid == 0) advance(segs[si ^ 1]);
 
         // ---- queries ----
         uint32_t qf[C::kQRegs ? P : 1][C::kQRegs ? NT : 1][KS][2];
@@ -356,8 +419,6 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                 continue;
             }
             const uint8_t *ub = ca_smem + (ring - sb) + st * C::kUnitBytes;
-            const bool two = key0 + 16 < s.kv;
-
             float sc[2][NT][4];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -366,51 +427,58 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sc[k][j][e] = 0.f;
             // ---- S^T = K Q^T: a lane holds tokens r, r + 8, channels t D / 4 .. ----
+            // (a second block past the sequence was not copied: what lies there is masked below)
+            uint32_t w[2][2][D / 32];
+            Scale2 ks[2][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (k == 1 && !two) break;
-                const uint8_t *blk = ub + k * B::kBytes;
-                uint32_t w[2][D / 32];
-                Scale2 s2[2];
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    const uint8_t *blk = ub + k * B::kBytes;
                     if constexpr (D == 128) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(blk + B::k_codes(r + 8 * h) + t * 16);
-                        w[h][0] = v.x;
-                        w[h][1] = v.y;
-                        w[h][2] = v.z;
-                        w[h][3] = v.w;
+                        w[k][h][0] = v.x;
+                        w[k][h][1] = v.y;
+                        w[k][h][2] = v.z;
+                        w[k][h][3] = v.w;
                     } else {
                         const uint2 v = *reinterpret_cast<const uint2 *>(blk + B::k_codes(r + 8 * h) + t * 8);
-                        w[h][0] = v.x;
-                        w[h][1] = v.y;
+                        w[k][h][0] = v.x;
+                        w[k][h][1] = v.y;
                     }
                     const uint32_t pr =
                         *reinterpret_cast<const uint32_t *>(blk + B::k_pair(r + 8 * h, t * (D / 4) / 32));
-                    s2[h] = scale2(prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232));
+                    ks[k][h] = scale2(prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232));
                 }
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t n0[4], n1[4];
-                    stored8(w[0][x], s2[0], n0);
-                    stored8(w[1][x], s2[1], n1);
+            for (int x = 0; x < D / 32; ++x) {
+                uint32_t n[2][2][4];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {   // contraction step 2 x + y
-                        const uint32_t a[4] = {n0[2 * y], n1[2 * y], n0[2 * y + 1], n1[2 * y + 1]};
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
+                    for (int h = 0; h < 2; ++h) stored8(w[k][h][x], ks[k][h], n[k][h]);
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                if constexpr (C::kQRegs) {
-                                    mma16816(sc[k][j], a, qf[p][j][2 * x + y]);
-                                } else {
-                                    const uint2 v = q_sm[((p * NT + j) * KS + 2 * x + y) * 32 + lane];
-                                    const uint32_t bq[2] = {v.x, v.y};
-                                    mma16816(sc[k][j], a, bq);
-                                }
+                for (int y = 0; y < 2; ++y)   // contraction step 2 x + y
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            uint32_t bq[2];
+                            if constexpr (C::kQRegs) {
+                                bq[0] = qf[p][j][2 * x + y][0];
+                                bq[1] = qf[p][j][2 * x + y][1];
+                            } else {
+                                const uint2 v = q_sm[((p * NT + j) * KS + 2 * x + y) * 32 + lane];
+                                bq[0] = v.x;
+                                bq[1] = v.y;
                             }
-                    }
-                }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t a[4] = {n[k][0][2 * y], n[k][1][2 * y], n[k][0][2 * y + 1],
+                                                       n[k][1][2 * y + 1]};
+                                mma16816(sc[k][j], a, bq);
+                            }
+                        }
             }
 
             // ---- softmax: element (token r + 8 (e / 2), row 2 t + (e & 1)) ----
@@ -479,7 +547,6 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
             // ---- O^T += V^T P^T: a lane holds channels r D / 8 .., tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 ----
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if (k == 1 && !two) break;
                 const uint8_t *blk = ub + k * B::kBytes;
                 uint32_t x[2][D / 32];   // 4 channels of a token pair each
                 Scale2 s2[2];
@@ -526,8 +593,10 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
         T_ += n_run;
 
         // ---- join the warps' rows, 8 at a time, and write them ----
-        const bool whole = k0 == 0 && cnt == units;
-        float *slot = slots + (k0 > 0 ? 0 : C::kSlot);   // cut before: slot 0; only after: slot 1
+        const bool whole = k0 == 0 && cnt == seg.units;
+        // cut before: slot 0; only after: slot 1
+        float *slot = reinterpret_cast<float *>(io.ws + gridDim.x * sizeof(CaDesc)) +
+                      ((size_t)blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * C::kSlot;
         float *mg = reinterpret_cast<float *>(ca_smem);
         float *mg_m = mg + kCaWarps * 8 * C::kMergeRow, *mg_l = mg_m + kCaWarps * 8;
         __syncthreads();   // every ring has been read
@@ -584,26 +653,25 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // plain writes above, copies next
         __syncthreads();
-        u += cnt;
-        off += cnt;
-        first = false;
     }
     if (failed && lane == 0) set_status(c.status, kDevTimeout);
 }
 
 // Joins the items that the cuts between CTAs divided.  Block (c, y) looks at
 // the cut before CTA c: it acts if that is the first cut inside its item, on
-// 8 / W of the item's RB rows, W warps a row.  The parts lie in the CTAs' slots:
-// slot 1 of CTA c - 1, where the item began, and slot 0 of c, c + 1, ...
-// Few rows have many parts (a long cache over the whole device): W = 4.
+// row y, y + gridDim.y, ... of the item's RB.  The parts lie in the CTAs' slots:
+// slot 1 of CTA c - 1, where the item began, and slot 0 of c, c + 1, ...  Latency
+// bounds it: all weights are loaded at once, then each warp has several parts
+// of its share in flight.
 constexpr int kJoinThreads = 256;
 
-template <typename T, int D, int RB, int W>
+template <typename T, int D, int RB>
 __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const CacheParams c, const CacheAttendIo io, int ctas)
 {
-    constexpr int V = D / 32;   // channels per lane
+    constexpr int V = D / 32, W = kJoinThreads / 32;   // channels per lane; warps
     constexpr int kSlot = RB * (D + 2);
-    __shared__ float part_o[8][D];
+    __shared__ float part_o[W][D], s_m[W], s_l[W];
+    __shared__ float weight[kJoinThreads];
     griddep_wait();
     const CaDesc *desc = reinterpret_cast<const CaDesc *>(io.ws);
     const float *slots = reinterpret_cast<const float *>(io.ws + ctas * sizeof(CaDesc));
@@ -614,44 +682,61 @@ __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const Cache
     if (item < ca_start(d.total, d.active, cta - 1)) return;   // not the item's first cut
     const int last = (int)(((item + d.units) * d.active - 1) / d.total);   // CTA of the item's last unit
     const int parts = last - cta + 2;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rr = blockIdx.y * (8 / W) + warp / W, sub = warp % W;
-    const int row = d.rb * RB + rr;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Seq s = load_seq(c, d.b);
     auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * kSlot; };
-    const bool ok = row < io.G * s.q;
-    float M = -INFINITY, L = 0.f;
-    float acc[V];
+    for (int rr = blockIdx.y; rr < RB; rr += gridDim.y) {   // block-uniform
+        const int row = d.rb * RB + rr;
+        if (row >= io.G * s.q) break;
+        float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    if (ok) {   // warp-uniform
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, part(p)[RB * D + rr]);
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        // online over batches of parts, one per thread (a device has fewer CTAs than a few batches)
+        for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {
+            const int p = p0 + tid;
+            const float m = p < parts ? part(p)[RB * D + rr] : -INFINITY, l = p < parts ? part(p)[RB * D + RB + rr] : 0.f;
+            float x = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float z = M == -INFINITY ? 0.f : M;
-        for (int p = lane; p < parts; p += 32)
-            L = fmaf(tc::fast_exp2(part(p)[RB * D + rr] - z), part(p)[RB * D + RB + rr], L);
+            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0) s_m[warp] = x;
+            __syncthreads();
+            float top = M;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
+            const float z = top == -INFINITY ? 0.f : top, f = tc::fast_exp2(m - z), g = tc::fast_exp2(M - z);
+            weight[tid] = f;
+            float y = f * l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if (lane == 0) s_l[warp] = y;
+            __syncthreads();
+            L *= g;
+#pragma unroll
+            for (int w = 0; w < W; ++w) L += s_l[w];
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] *= g;
+            M = top;
 #pragma unroll 8
-        for (int p = sub; p < parts; p += W) {
-            const float *q = part(p);
-            const float f = tc::fast_exp2(q[RB * D + rr] - z);
+            for (int i = warp; i < min(kJoinThreads, parts - p0); i += W) {
+                const float *q = part(p0 + i) + rr * D + lane * V;
+                const float wt = weight[i];
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(f, q[rr * D + lane * V + e], acc[e]);
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(wt, q[e], acc[e]);
+            }
+            __syncthreads();
         }
-    }
 #pragma unroll
-    for (int e = 0; e < V; ++e) part_o[warp][lane * V + e] = acc[e];
-    __syncthreads();
-    const int d4 = 4 * lane;
-    if (ok && sub == 0 && d4 < D) {
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int e = 0; e < V; ++e) part_o[warp][lane * V + e] = acc[e];
+        __syncthreads();
+        if (tid < D / 4) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+            for (int w = 0; w < W; ++w)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] += part_o[warp + w][d4 + e];
-        ca_write<T, D>(c, io, d.b, d.hkv, row, d4, make_float4(o[0], o[1], o[2], o[3]), M, L);
+                for (int e = 0; e < 4; ++e) o[e] += part_o[w][4 * tid + e];
+            ca_write<T, D>(c, io, d.b, d.hkv, row, 4 * tid, make_float4(o[0], o[1], o[2], o[3]), M, L);
+        }
+        __syncthreads();
     }
 }
 

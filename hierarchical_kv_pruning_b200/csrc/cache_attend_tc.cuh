@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             all_items += s_items[w];
         }
         const long long ctas = gridDim.x;
-        const bool whole = (all_items + ctas - 1) / ctas * top <= (total + ctas - 1) / ctas + kPartialUnits;
+        const bool whole = ca_whole(all_items, ctas, top, total, kPartialUnits);
         const int active = (int)max(1LL, min(ctas, total));
         if (!whole && (total == 0 || blockIdx.x >= active)) return;   // CTA-uniform
         if (tid == 0) {
