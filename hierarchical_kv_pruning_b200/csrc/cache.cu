@@ -205,6 +205,14 @@ size_t ca_workspace(const atlaskv_cache *c)
     return n * sizeof(akv::CaDesc) + n * 2 * akv::Ca<T, D, NT>::kSlot * sizeof(float);
 }
 
+// Blocks of the join: as many divided items as there can be, each by as many
+// blocks as make about one wave (blocks that find nothing to do cost, too).
+dim3 join_grid(long long items, int ctas, int rows)
+{
+    const int x = (int)std::min<long long>(items, ctas - 1);
+    return dim3(std::max(1, x), std::max(1, std::min(rows, 592 / std::max(1, x))));
+}
+
 template <typename T, int D, int NT>
 atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, const akv::CacheAttendIo &a, cudaStream_t s)
 {
@@ -215,7 +223,8 @@ atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, cons
     // no cuts whatever the lengths are: no join
     const long long items = (long long)p.B * p.H_kv * (((long long)p.N * a.G + C::kRB - 1) / C::kRB);
     if (akv::ca_whole(items, n, slots_of(p) / akv::kCaUnit + 1, 0, akv::kCaPartialUnits)) return ATLASKV_OK;
-    return launch_pdl(akv::cache_combine_kernel<T, D, C::kRB>, dim3(n - 1, 8), akv::kJoinThreads, 0, s, p, a, n);
+    return launch_pdl(akv::cache_combine_kernel<T, D, C::kRB>, join_grid(items, n, C::kRB), akv::kJoinThreads, 0, s, p, a,
+                      n);
 }
 
 // Many rows of bfloat16 queries: tcgen05 (the few-rows kernel would turn the
@@ -238,8 +247,10 @@ atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, cons
     const int n = c->num_sms;
     AKV_RET(launch_pdl(akv::cache_attend_tc_kernel<D>, dim3(n), akv::ctc::kThreads, akv::ctc::Smem<D>::kBytes, s, p, a,
                        (int)nb));
-    if (akv::ca_whole(nb * p.B * p.H_kv, n, slots_of(p) / akv::ctc::kKeys + 1, 0, akv::ctc::kPartialUnits)) return ATLASKV_OK;
-    return launch_pdl(akv::cache_combine_kernel<__nv_bfloat16, D, RB>, dim3(n - 1, 32), akv::kJoinThreads, 0, s, p, a, n);
+    const long long items = nb * p.B * p.H_kv;
+    if (akv::ca_whole(items, n, slots_of(p) / akv::ctc::kKeys + 1, 0, akv::ctc::kPartialUnits)) return ATLASKV_OK;
+    return launch_pdl(akv::cache_combine_kernel<__nv_bfloat16, D, RB>, join_grid(items, n, RB), akv::kJoinThreads, 0, s, p,
+                      a, n);
 }
 
 // f<T, D, NT>(args...) for the call's type, head dimension and rows
@@ -358,7 +369,7 @@ atlaskv_status atlaskv_create_cache(const atlaskv_cache_desc *d, void *stream, a
     c->d = *d;
     const auto init = [&]() -> atlaskv_status {
         AKV_CUDA(cudaGetDevice(&c->device));
-        c->num_sms = num_sms();
+        c->num_sms = std::min(num_sms(), akv::kMaxCtas / 4);
         AKV_CUDA(cudaMalloc(&c->status, sizeof(int)));
         AKV_CUDA(cudaMemsetAsync(c->status, 0, sizeof(int), static_cast<cudaStream_t>(stream)));
         AKV_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));

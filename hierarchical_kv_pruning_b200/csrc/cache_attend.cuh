@@ -85,9 +85,9 @@ struct Ca {
     static constexpr int kSlot = kRB * (D + 2);             // floats of a partial: O, m, l
 };
 
-// A divided item costs about as much as this many units more on every CTA (the
-// partials, a second launch's work: about 4 us against 0.1 us a unit of a CTA).
-constexpr int kCaPartialUnits = 40;
+// A divided item costs about as much as this many units more on every CTA: the
+// join takes about 4 us, four units (one a warp) about 1.1 us where a warp is alone.
+constexpr int kCaPartialUnits = 20;
 
 // Whether whole items, round-robin over the CTAs, end about as early as equal
 // runs of units would.
@@ -107,8 +107,8 @@ struct CaDesc {
 
 // A CTA's walk over its runs of units, kept in shared memory by one thread.
 struct CaWalk {
-    long long total, u, end, off;   // units of the call; next unit and the run's end; the next one's offset within b
-    int active, whole, b;           // CTAs with units; whole items (off counts items, u and end do not matter)?
+    long long total, u, end, off;   // units of the call; next unit (item) and the end; its offset within sequence b
+    int active, whole, b;           // CTAs with units; whole items?
 };
 
 // One stretch of an item's units.
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
     __shared__ int s_top[kCaWarps];
     __shared__ CaWalk walk;
     __shared__ CaSeg segs[2];
+    __shared__ long long s_first[kCaThreads + 1];   // items before thread t's sequences
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, t = lane & 3;
     const uint32_t sb = tc::smem_addr(ca_smem);
     const uint32_t ring = sb + warp * S * C::kUnitBytes, bars = sb + C::kOffBar + warp * S * 8;
@@ -210,29 +211,36 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
         mine += n * n_units(s);
         top = max(top, n > 0 ? n_units(s) : 0);
     }
-    long long scan = mine;
+    long long scan = mine, iscan = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += v;
-        items += __shfl_xor_sync(0xffffffffu, items, o);
+        const long long v = __shfl_up_sync(0xffffffffu, scan, o), x = __shfl_up_sync(0xffffffffu, iscan, o);
+        if (lane >= o) {
+            scan += v;
+            iscan += x;
+        }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
     if (lane == 31) {
         s_sum[warp] = scan;
-        s_items[warp] = items;
+        s_items[warp] = iscan;
         s_top[warp] = top;
     }
     __syncthreads();
-    long long total = 0, before = scan - mine, all = 0;
+    long long total = 0, before = scan - mine, all = 0, ibefore = iscan - items;
     int longest = 0;
 #pragma unroll
     for (int w = 0; w < kCaWarps; ++w) {
-        if (w < warp) before += s_sum[w];
+        if (w < warp) {
+            before += s_sum[w];
+            ibefore += s_items[w];
+        }
         total += s_sum[w];
         all += s_items[w];
         longest = max(longest, s_top[w]);
     }
+    s_first[tid] = ibefore;
+    if (tid == 0) s_first[kCaThreads] = all;
     CaDesc *desc = reinterpret_cast<CaDesc *>(io.ws) + blockIdx.x;
     if (tid == 0) desc->k0 = 0;   // until the CTA begins inside an item
     {
@@ -248,15 +256,25 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                 if (off < n) break;
                 off -= n;
             }
-            walk = CaWalk{total, u, ca_start(total, active, blockIdx.x + 1), whole ? blockIdx.x : off, active, whole,
-                          whole ? 0 : b};
+            walk = CaWalk{total, whole ? blockIdx.x : u, whole ? all : ca_start(total, active, blockIdx.x + 1), off, active,
+                          whole, b};
         }
     }
     // the next stretch, by one thread: while the CTA is busy with the one before
     auto advance = [&](CaSeg &g) {
         CaWalk w = walk;
         g.cnt = 0;
-        while (w.b < c.B && (w.whole || w.u < w.end)) {
+        if (w.whole) {   // item w.u: the thread whose sequences hold it, then its place among them
+            if (w.u >= s_first[kCaThreads]) return;
+            int lo = 0, hi = kCaThreads;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                (s_first[mid] <= w.u ? lo : hi) = mid;
+            }
+            w.b = lo * per;
+            w.off = w.u - s_first[lo];
+        }
+        while (w.b < c.B && w.u < w.end) {
             const Seq s = load_seq(c, w.b);
             const int nb = n_blocks(s), units = n_units(s);
             const long long n = (long long)c.H_kv * nb * (w.whole ? 1 : units);
@@ -273,8 +291,8 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
             g.units = units;
             g.k0 = w.whole ? 0 : (int)(w.off - (long long)item * units);
             g.cnt = w.whole ? units : (int)min((long long)(units - g.k0), w.end - w.u);
-            w.u += g.cnt;
-            w.off += w.whole ? gridDim.x : g.cnt;
+            w.u += w.whole ? gridDim.x : g.cnt;
+            w.off += g.cnt;
             break;
         }
         walk = w;
@@ -657,13 +675,14 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
     if (failed && lane == 0) set_status(c.status, kDevTimeout);
 }
 
-// Joins the items that the cuts between CTAs divided.  Block (c, y) looks at
-// the cut before CTA c: it acts if that is the first cut inside its item, on
-// row y, y + gridDim.y, ... of the item's RB.  The parts lie in the CTAs' slots:
+// Joins the items that the cuts between CTAs divided: block (x, y) the x-th of
+// them (every gridDim.x-th), rows y, y + gridDim.y, ... of its RB.  An item is
+// found at its first cut: the cut before CTA c is one if the item that CTA c
+// begins inside of began in CTA c - 1's run.  The parts lie in the CTAs' slots:
 // slot 1 of CTA c - 1, where the item began, and slot 0 of c, c + 1, ...  Latency
-// bounds it: all weights are loaded at once, then each warp has several parts
-// of its share in flight.
-constexpr int kJoinThreads = 256;
+// bounds it: all cuts are looked at at once, all weights loaded at once, and
+// each warp has several parts of its share in flight.
+constexpr int kJoinThreads = 256, kMaxCtas = 2048;
 
 template <typename T, int D, int RB>
 __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const CacheParams c, const CacheAttendIo io, int ctas)
@@ -672,71 +691,93 @@ __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const Cache
     constexpr int kSlot = RB * (D + 2);
     __shared__ float part_o[W][D], s_m[W], s_l[W];
     __shared__ float weight[kJoinThreads];
+    __shared__ int16_t firsts[kMaxCtas];               // the first cuts, in order
+    __shared__ int counts[W];
     griddep_wait();
-    const CaDesc *desc = reinterpret_cast<const CaDesc *>(io.ws);
+    const CaDesc *descs = reinterpret_cast<const CaDesc *>(io.ws);
     const float *slots = reinterpret_cast<const float *>(io.ws + ctas * sizeof(CaDesc));
-    const int cta = blockIdx.x + 1;
-    const CaDesc d = desc[cta];
-    if (d.k0 == 0) return;                              // no item divided here
-    const long long u = ca_start(d.total, d.active, cta), item = u - d.k0;
-    if (item < ca_start(d.total, d.active, cta - 1)) return;   // not the item's first cut
-    const int last = (int)(((item + d.units) * d.active - 1) / d.total);   // CTA of the item's last unit
-    const int parts = last - cta + 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Seq s = load_seq(c, d.b);
-    auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * kSlot; };
-    for (int rr = blockIdx.y; rr < RB; rr += gridDim.y) {   // block-uniform
-        const int row = d.rb * RB + rr;
-        if (row >= io.G * s.q) break;
-        float M = -INFINITY, L = 0.f, acc[V];
+    int n_first = 0;
+    for (int base = 1; base < ctas; base += kJoinThreads) {
+        const int x = base + tid;
+        bool first = false;
+        if (x < ctas) {
+            const CaDesc d = descs[x];
+            first = d.k0 > 0 && ca_start(d.total, d.active, x) - d.k0 >= ca_start(d.total, d.active, x - 1);
+        }
+        const unsigned vote = __ballot_sync(0xffffffffu, first);
+        if (lane == 0) counts[warp] = __popc(vote);
+        __syncthreads();
+        int at = n_first + __popc(vote & ((1u << lane) - 1));
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
-        // online over batches of parts, one per thread (a device has fewer CTAs than a few batches)
-        for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {
-            const int p = p0 + tid;
-            const float m = p < parts ? part(p)[RB * D + rr] : -INFINITY, l = p < parts ? part(p)[RB * D + RB + rr] : 0.f;
-            float x = m;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) at += counts[w];
+            n_first += counts[w];
+        }
+        if (first) firsts[at] = (int16_t)x;
+        __syncthreads();
+    }
+    for (int fi = blockIdx.x; fi < n_first; fi += gridDim.x) {   // block-uniform
+        const int cta = firsts[fi];
+        const CaDesc d = descs[cta];
+        const long long item = ca_start(d.total, d.active, cta) - d.k0;
+        const int last = (int)(((item + d.units) * d.active - 1) / d.total);   // CTA of the item's last unit
+        const int parts = last - cta + 2;
+        const Seq s = load_seq(c, d.b);
+        auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * kSlot; };
+        for (int rr = blockIdx.y; rr < RB; rr += gridDim.y) {   // block-uniform
+            const int row = d.rb * RB + rr;
+            if (row >= io.G * s.q) break;
+            float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (lane == 0) s_m[warp] = x;
-            __syncthreads();
-            float top = M;
+            for (int e = 0; e < V; ++e) acc[e] = 0.f;
+            // online over batches of parts, one per thread (a device has fewer CTAs than a few batches)
+            for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {
+                const int p = p0 + tid;
+                const float m = p < parts ? part(p)[RB * D + rr] : -INFINITY, l = p < parts ? part(p)[RB * D + RB + rr] : 0.f;
+                float x = m;
 #pragma unroll
-            for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
-            const float z = top == -INFINITY ? 0.f : top, f = tc::fast_exp2(m - z), g = tc::fast_exp2(M - z);
-            weight[tid] = f;
-            float y = f * l;
+                for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if (lane == 0) s_m[warp] = x;
+                __syncthreads();
+                float top = M;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (lane == 0) s_l[warp] = y;
-            __syncthreads();
-            L *= g;
+                for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
+                const float z = top == -INFINITY ? 0.f : top, f = tc::fast_exp2(m - z), g = tc::fast_exp2(M - z);
+                weight[tid] = f;
+                float y = f * l;
 #pragma unroll
-            for (int w = 0; w < W; ++w) L += s_l[w];
+                for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                if (lane == 0) s_l[warp] = y;
+                __syncthreads();
+                L *= g;
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] *= g;
-            M = top;
+                for (int w = 0; w < W; ++w) L += s_l[w];
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] *= g;
+                M = top;
 #pragma unroll 8
-            for (int i = warp; i < min(kJoinThreads, parts - p0); i += W) {
-                const float *q = part(p0 + i) + rr * D + lane * V;
-                const float wt = weight[i];
+                for (int i = warp; i < min(kJoinThreads, parts - p0); i += W) {
+                    const float *q = part(p0 + i) + rr * D + lane * V;
+                    const float wt = weight[i];
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = fmaf(wt, q[e], acc[e]);
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(wt, q[e], acc[e]);
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) part_o[warp][lane * V + e] = acc[e];
+            __syncthreads();
+            if (tid < D / 4) {
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] += part_o[w][4 * tid + e];
+                ca_write<T, D>(c, io, d.b, d.hkv, row, 4 * tid, make_float4(o[0], o[1], o[2], o[3]), M, L);
             }
             __syncthreads();
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) part_o[warp][lane * V + e] = acc[e];
-        __syncthreads();
-        if (tid < D / 4) {
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] += part_o[w][4 * tid + e];
-            ca_write<T, D>(c, io, d.b, d.hkv, row, 4 * tid, make_float4(o[0], o[1], o[2], o[3]), M, L);
-        }
-        __syncthreads();
     }
 }
 
