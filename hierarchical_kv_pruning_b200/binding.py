@@ -36,7 +36,7 @@ EXPORTED = ("atlaskv_create_tree", "atlaskv_workspace_size", "atlaskv_attend", "
             "atlaskv_set_descent", "atlaskv_set_leaf_cache", "atlaskv_leaf_cache_stats", "atlaskv_rope_init",
             "atlaskv_rope", "atlaskv_cache_page_bytes", "atlaskv_create_cache", "atlaskv_destroy_cache",
             "atlaskv_cache_sync_status", "atlaskv_cache_append", "atlaskv_cache_read", "atlaskv_cache_workspace_size",
-            "atlaskv_cache_attend")
+            "atlaskv_cache_attend", "atlaskv_workspace_size_cached", "atlaskv_attend_cached")
 MAX_LAYERS = 32
 MAX_LEVELS = 4
 # Size of the library's static device scratch (ATLASKV_STATIC_SCRATCH_BYTES).
@@ -187,6 +187,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             lib.atlaskv_cache_read.argtypes = [V, SEQS, I32, V, V, V]
             lib.atlaskv_cache_workspace_size.argtypes = [V, I32, I32, I32, I32, ctypes.POINTER(SZ)]
             lib.atlaskv_cache_attend.argtypes = [V, SEQS, ctypes.POINTER(atlaskv_cache_attend_io), V, SZ, V]
+            lib.atlaskv_workspace_size_cached.argtypes = [V, ctypes.POINTER(atlaskv_params), V, I32, I32, I32,
+                                                          ctypes.POINTER(SZ)]
+            lib.atlaskv_attend_cached.argtypes = [V, ctypes.POINTER(atlaskv_params), ctypes.POINTER(atlaskv_io), V, SEQS,
+                                                  V, SZ, V]
             lib.atlaskv_last_error.argtypes = []
             lib.atlaskv_last_error.restype = ctypes.c_char_p
             for name in EXPORTED:
@@ -380,6 +384,18 @@ def atlaskv_cache_attend(cache: int, seqs: atlaskv_seqs, io: atlaskv_cache_atten
                                                workspace_bytes, stream))
 
 
+def atlaskv_workspace_size_cached(tree: int, params: atlaskv_params, cache: int, B: int, N: int, H: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().atlaskv_workspace_size_cached(tree, ctypes.byref(params), cache, B, N, H, ctypes.byref(out)))
+    return out.value
+
+
+def atlaskv_attend_cached(tree: int, params: atlaskv_params, io: atlaskv_io, cache: int, seqs: atlaskv_seqs,
+                          workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().atlaskv_attend_cached(tree, ctypes.byref(params), ctypes.byref(io), cache,
+                                                ctypes.byref(seqs), workspace, workspace_bytes, stream))
+
+
 # ---- torch-facing convenience ------------------------------------------------
 
 def _dtype_code(t: torch.dtype) -> int:
@@ -485,6 +501,39 @@ class HikvpTree:
         io = atlaskv_io(B, N, H, T, _ptr(q_kg), _ptr(q_seq), _ptr(k_seq), _ptr(v_seq), _ptr(out), _ptr(lse),
                         _ptr(kept[0]), _ptr(kept[1]), _ptr(kept[2]))
         atlaskv_attend(self.handle, p, io, workspace.data_ptr(), workspace.numel(), _stream(stream))
+        return {"out": out, "lse": lse, "kept_root": kept[0], "kept_mid": kept[1], "kept_leaf": kept[2],
+                "workspace": workspace}
+
+    def attend_cached(self, q_kg, q_seq, cache: "KvCache", block_table, kv_len, K, scale: float = 0.0, out=None, lse=None,
+                      kept=None, workspace=None, want_kept: bool = True, want_lse: bool = True, stream=None):
+        """attend() with the sequence's keys and values in `cache` (kv_len [B]
+        stored tokens, the N query tokens being the newest).  Returns the same dict."""
+        B, N, H, D = q_kg.shape
+        p, new = self.params(K, scale), []
+
+        def alloc(shape, dtype):
+            new.append(torch.empty(shape, dtype=dtype, device=q_kg.device))
+            return new[-1]
+
+        if out is None:
+            out = alloc(q_kg.shape, q_kg.dtype)
+        if want_lse and lse is None:
+            lse = alloc((B, N, H), torch.float32)
+        if want_kept and kept is None:
+            kept = tuple(alloc((B, H, int(k)), torch.int32) for k in K)
+        if kept is None:
+            kept = (None, None, None)
+        if workspace is None:
+            nbytes = atlaskv_workspace_size_cached(self.handle, p, cache.handle, B, N, H)
+            workspace = alloc((max(nbytes, 256),), torch.uint8)
+        s = _on_device(cache._index, stream, q_kg, q_seq, block_table, kv_len, out, lse, workspace, *kept)
+        shape = (B, N, H, D)
+        io = atlaskv_io(B, N, H, N, _dense("q_kg", q_kg, shape, self.dtype), _dense("q_seq", q_seq, shape, self.dtype),
+                        None, None, _dense("out", out, shape, self.dtype), _ptr(lse), _ptr(kept[0]), _ptr(kept[1]),
+                        _ptr(kept[2]))
+        atlaskv_attend_cached(self.handle, p, io, cache.handle, cache._seqs(B, N, block_table, kv_len, None),
+                              workspace.data_ptr(), workspace.nbytes, s)
+        _used_on(stream, *new)
         return {"out": out, "lse": lse, "kept_root": kept[0], "kept_mid": kept[1], "kept_leaf": kept[2],
                 "workspace": workspace}
 

@@ -354,7 +354,10 @@ bool use_pm(const atlaskv_tree *t, bool pm_ok, bool fused_ok, long long BH)
     return pm_ok && (!fused_ok || BH >= kPmAutoMinTraversals);
 }
 
-Layout plan(const atlaskv_tree *t, const Ks &ks, int B, int N, int H, int T, bool allow_pm = true)
+// seq_apart: the sequence part has a launch of its own whatever the tree says
+// (its keys and values come from a cache).
+Layout plan(const atlaskv_tree *t, const Ks &ks, int B, int N, int H, int T, bool allow_pm = true,
+            bool seq_apart = false)
 {
     (void)N;
     (void)T;
@@ -389,7 +392,7 @@ Layout plan(const atlaskv_tree *t, const Ks &ks, int B, int N, int H, int T, boo
     L.xs = take(L.pm ? BH * akv::ExactScratch::bytes()
                      : (size_t)B * t->d.n_kv_heads * (G / gc) * std::max(1, L.desc.nsel) * akv::ExactScratch::bytes());
     for (int l = 0; l < ks.n; ++l) L.kept[l] = take(BH * (size_t)ks.K[l] * 4);
-    if (t->split) {   // the sequence part's normalised output and log-sum-exp, fp32
+    if (t->split || seq_apart) {   // the sequence part's normalised output and log-sum-exp, fp32
         L.oseq = take(BH * (size_t)N * D * 4);
         L.lse_seq = take(BH * (size_t)N * 4);
     }
@@ -868,7 +871,7 @@ struct Call {
 // Descent and attention parameters of one call on tree t with workspace ws;
 // kept_out[l]: the caller's kept-id buffer of level l, or null.
 void fill_call(const atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, int32_t *const *kept_out, uint8_t *ws,
-               Call &c)
+               Call &c, bool seq_apart = false)
 {
     const Layout &L = c.L;
     const int D = t->d.head_dim;
@@ -936,7 +939,7 @@ void fill_call(const atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, int32_
     ap.K_L = ks.K[nl - 1];
     ap.scale_log2 = scale * 1.4426950408889634f;
     ap.status = t->status;
-    if (t->split) {
+    if (t->split || seq_apart) {
         ap.oseq = reinterpret_cast<float *>(ws + L.oseq);
         ap.lse_seq = reinterpret_cast<float *>(ws + L.lse_seq);
     }
@@ -1288,8 +1291,15 @@ atlaskv_status atlaskv_create_tree_csr(const atlaskv_csr_tree_desc *d, void *str
 }
 
 namespace {
+// The sequence part's keys and values in a paged cache instead of io->k_seq / v_seq.
+struct CachedSeq {
+    atlaskv_cache *cache;
+    const atlaskv_seqs *seqs;
+    size_t ws_bytes;   // of its launches, behind the call's own
+};
+
 atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, int32_t *const *kept_out,
-                           void *workspace, size_t ws_bytes, void *stream);
+                           void *workspace, size_t ws_bytes, void *stream, const CachedSeq *cs = nullptr);
 
 Ks ks_of_levels(const atlaskv_tree *t, const atlaskv_level_params *p)
 {
@@ -1343,7 +1353,7 @@ namespace {
 // The whole path for one call (uniform or CSR tree); kept_out[l] is the
 // caller's kept-id buffer of level l, or null.
 atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, int32_t *const *kept_out,
-                           void *workspace, size_t ws_bytes, void *stream)
+                           void *workspace, size_t ws_bytes, void *stream, const CachedSeq *cs)
 {
     if (!io) return fail(ATLASKV_EINVAL, "null io");
     atlaskv_status st = check_params(t, ks, io->B, io->N, io->H, io->T);
@@ -1352,11 +1362,12 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
     st = check_io(io);
     if (st != ATLASKV_OK) return st;
     Call call;
-    call.L = plan(t, ks, io->B, io->N, io->H, io->T);
+    call.L = plan(t, ks, io->B, io->N, io->H, io->T, true, cs != nullptr);
     const Layout &L = call.L;
+    const size_t need = L.total + (cs ? cs->ws_bytes : 0);
     if (!workspace || ((uintptr_t)workspace & 255u)) return fail(ATLASKV_EINVAL, "workspace must be 256-byte aligned");
-    if (ws_bytes < L.total)
-        return fail(ATLASKV_ENOMEM, "workspace of %zu bytes, %zu needed", ws_bytes, L.total);
+    if (ws_bytes < need)
+        return fail(ATLASKV_ENOMEM, "workspace of %zu bytes, %zu needed", ws_bytes, need);
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
@@ -1364,7 +1375,7 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
     const int H_kv = t->d.n_kv_heads;
     const int G = io->H / H_kv;
     const bool host = t->host_leaves;
-    fill_call(t, ks, io, kept_out, ws, call);
+    fill_call(t, ks, io, kept_out, ws, call, cs != nullptr);
     akv::DescendParams &dp = call.dp;
     akv::AttnParams &ap = call.ap;
     int32_t *const *kept = call.kept;
@@ -1386,8 +1397,19 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
     // The sequence part depends only on the call's inputs: with the split it
     // starts at once on the tree's low-priority stream, beside the descent
     // (and the staging), and the leaf part merges with it afterwards.
+    auto cached_part = [&](cudaStream_t st) -> atlaskv_status {
+        return akv_cache_part(cs->cache, cs->seqs, t->d.dtype, io->H, io->q_seq, ks.scale, ap.oseq, ap.lse_seq,
+                              ws + L.total, cs->ws_bytes, st);
+    };
     auto fork_sequence_part = [&]() -> atlaskv_status {
         AKV_CUDA(cudaStreamWaitEvent(t->seq_stream, t->fev[0], 0));
+        if (cs) {
+            AKV_STEP(tm(2, t->seq_stream));
+            AKV_STEP(cached_part(t->seq_stream));
+            AKV_STEP(tm(3, t->seq_stream));
+            AKV_CUDA(cudaEventRecord(t->fev[2], t->seq_stream));
+            return ATLASKV_OK;
+        }
         akv::AttnParams a = ap;
         a.mode = akv::kAttnSeq;
         AKV_STEP(tm(2, t->seq_stream));
@@ -1422,6 +1444,10 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
             AKV_STEP(dispatch_attend(t->d.dtype, D, ap, s));
             AKV_STEP(tm(5, s));
         } else {
+            if (cs) {
+                AKV_STEP(cached_part(s));
+                ap.mode = akv::kAttnLeaf;
+            }
             AKV_STEP(tm(0, s));
             AKV_STEP(descend_all(s));
             AKV_STEP(tm(1, s));
@@ -1514,7 +1540,7 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
             a.leaf_head_stride = 0;
             a.lk_rows = (long long)k.groups * n_mid * t->d.fanout[2];
             a.lv_rows = (long long)k.groups * n_leaf;
-            if (t->split) a.mode = akv::kAttnLeaf;
+            if (t->split || cs) a.mode = akv::kAttnLeaf;
             k.a = a;
         }
         // The pipeline of one chunk: descent ranges on the caller's stream
@@ -1543,6 +1569,8 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
         if (t->split) {
             AKV_CUDA(cudaEventRecord(t->fev[0], s));
             AKV_STEP(fork_sequence_part());
+        } else if (cs) {
+            AKV_STEP(cached_part(s));
         }
         if (t->cache_pool) ++t->cache_epoch;   // this call's stamp (epoch 0 marks empty ways)
         for (int k = 0; k < np; ++k) {
@@ -1612,6 +1640,57 @@ atlaskv_status atlaskv_attend(atlaskv_tree *t, const atlaskv_params *p, const at
     if (t && t->csr) return fail(ATLASKV_EINVAL, "a CSR tree is attended with atlaskv_attend_csr");
     int32_t *kept[3] = {io->kept_root, io->kept_mid, io->kept_leaf};
     return attend_impl(t, ks_of(p), io, kept, workspace, ws_bytes, stream);
+}
+
+// ---- the sequence in a paged cache --------------------------------------------
+namespace {
+
+// Checks of the two cached entry points; on OK *cs describes the sequence part.
+atlaskv_status check_cached(const atlaskv_tree *t, const atlaskv_params *p, atlaskv_cache *cache, int B, int N, int H,
+                            CachedSeq *cs)
+{
+    if (!t || !p || !cache) return fail(ATLASKV_EINVAL, "null tree, params or cache");
+    if (t->csr) return fail(ATLASKV_EUNSUPPORTED, "a cached sequence with a CSR tree");
+    AKV_RET(check_params(t, ks_of(p), B, N, H, N));
+    AKV_RET(akv_cache_matches(cache, t->d.n_kv_heads, t->d.head_dim));
+    size_t bytes = 0;
+    AKV_RET(atlaskv_cache_workspace_size(cache, t->d.dtype, B, N, H, &bytes));
+    cs->cache = cache;
+    cs->ws_bytes = align256(bytes);
+    return ATLASKV_OK;
+}
+
+}  // namespace
+
+atlaskv_status atlaskv_workspace_size_cached(const atlaskv_tree *t, const atlaskv_params *p, const atlaskv_cache *cache,
+                                             int32_t B, int32_t N, int32_t H, size_t *bytes)
+{
+    if (!bytes) return fail(ATLASKV_EINVAL, "null bytes");
+    CachedSeq cs{};
+    AKV_RET(check_cached(t, p, const_cast<atlaskv_cache *>(cache), B, N, H, &cs));
+    *bytes = plan(t, ks_of(p), B, N, H, N, true, true).total + cs.ws_bytes;
+    return ATLASKV_OK;
+}
+
+atlaskv_status atlaskv_attend_cached(atlaskv_tree *t, const atlaskv_params *p, const atlaskv_io *io,
+                                     atlaskv_cache *cache, const atlaskv_seqs *seqs, void *workspace, size_t ws_bytes,
+                                     void *stream)
+{
+    if (!io || !seqs) return fail(ATLASKV_EINVAL, "null io or seqs");
+    CachedSeq cs{};
+    AKV_RET(check_cached(t, p, cache, io->B, io->N, io->H, &cs));
+    if (seqs->B != io->B || seqs->N != io->N)
+        return fail(ATLASKV_EINVAL, "seqs (B = %d, N = %d) and io (B = %d, N = %d) differ", seqs->B, seqs->N, io->B, io->N);
+    if (seqs->q_len) return fail(ATLASKV_EINVAL, "q_len must be NULL: every query has N tokens");
+    if (io->B == 0) return ATLASKV_OK;
+    if (!seqs->block_table || !seqs->kv_len || seqs->max_pages < 1)
+        return fail(ATLASKV_EINVAL, "null block_table or kv_len, or max_pages < 1");
+    cs.seqs = seqs;
+    atlaskv_io x = *io;
+    x.T = x.N;                      // no sequence tensors: the knowledge part reads neither of these
+    x.k_seq = x.v_seq = x.q_seq;
+    int32_t *kept[3] = {io->kept_root, io->kept_mid, io->kept_leaf};
+    return attend_impl(t, ks_of(p), &x, kept, workspace, ws_bytes, stream, &cs);
 }
 
 // ---- several layers in one call ----------------------------------------------

@@ -28,9 +28,9 @@ struct AttnParams {
     int B, N, H, H_kv, G, T, K_L;
     float scale_log2;                // scale * log2(e)
     int *status;                     // sticky device status word (bounded waits report here)
-    // tensor-core kernel only: which key sets one launch covers (kAttn*), and
-    // the sequence part's results handed from the sequence launch to the leaf
-    // launch, per (query, KV head) group and group row r = g N + n
+    // which key sets one launch covers (kAttn*; kAttnSeq in the tensor-core
+    // kernel only), and the sequence part's results handed from the sequence
+    // launch to the leaf launch, per (query, KV head) group and group row r = g N + n
     int mode;
     float *oseq;                     // [B H_kv][G N][D] normalised sequence-part output
     float *lse_seq;                  // [B H_kv][G N] its log-sum-exp (natural log)
@@ -88,12 +88,21 @@ __global__ void __launch_bounds__(128) attend_f32_kernel(const AttnParams p)
         const long long rv = p.leaf_head_stride * hkv + p.lv_idx[bh * p.K_L + j];
         visit(lk + rk * D, lv + rv * D, a);
     }
-    const float *ks = reinterpret_cast<const float *>(p.k_seq);
-    const float *vs = reinterpret_cast<const float *>(p.v_seq);
-    const int last = p.T - p.N + n;
-    for (int i = 0; i <= last; ++i) {
-        const long long r = ((long long)b * p.T + i) * p.H_kv + hkv;
-        visit(ks + r * D, vs + r * D, c);
+    if (p.mode == kAttnLeaf) {   // the sequence part was its own launch: its rows weigh e^{lse_seq}
+        const long long g = ((long long)b * p.H_kv + hkv) * p.G * p.N + (long long)(h - hkv * p.G) * p.N + n;
+        const float s = p.lse_seq[g], mn = fmaxf(m, s), alpha = expf(m - mn), w = expf(s - mn);
+        l = l * alpha + w;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, p.oseq[g * D + lane + 32 * i], acc[i] * alpha);
+        m = mn;
+    } else {
+        const float *ks = reinterpret_cast<const float *>(p.k_seq);
+        const float *vs = reinterpret_cast<const float *>(p.v_seq);
+        const int last = p.T - p.N + n;
+        for (int i = 0; i <= last; ++i) {
+            const long long r = ((long long)b * p.T + i) * p.H_kv + hkv;
+            visit(ks + r * D, vs + r * D, c);
+        }
     }
     float *out = reinterpret_cast<float *>(p.out) + row * D;
     const float inv = 1.f / l;

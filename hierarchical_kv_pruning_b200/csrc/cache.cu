@@ -277,6 +277,37 @@ atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, cons
         }                                                                            \
     } while (0)
 
+// Attention over the cache into a.out / a.lse or a.oseq / a.lse_seq.
+atlaskv_status attend_cache(atlaskv_cache *c, const atlaskv_seqs *seqs, int dtype, int H, float scale,
+                            akv::CacheAttendIo a, void *workspace, size_t workspace_bytes, void *stream)
+{
+    AKV_RET(check_cache(c));
+    akv::CacheParams p;
+    AKV_RET(cache_params(c, seqs, &p));
+    size_t need = 0;
+    AKV_RET(atlaskv_cache_workspace_size(c, dtype, seqs->B, seqs->N, H, &need));
+    if (!(scale >= 0.f) || std::isinf(scale)) return fail(ATLASKV_EINVAL, "scale must be finite and >= 0");
+    if (seqs->B == 0) return ATLASKV_OK;
+    const int D = c->d.head_dim;
+    int64_t qs;
+    AKV_RET(check_rows("q", a.q, (int64_t)H * D, dtype, a.qs, &qs));
+    if (!a.oseq && (!a.out || !aligned16(a.out))) return fail(ATLASKV_EINVAL, "null or unaligned out");
+    if (a.lse && !aligned4(a.lse)) return fail(ATLASKV_EINVAL, "unaligned lse");
+    if (!workspace || ((uintptr_t)workspace & 255u)) return fail(ATLASKV_EINVAL, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(ATLASKV_ENOMEM, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    a.qs = qs;
+    a.H = H;
+    a.G = H / p.H_kv;
+    a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+    a.ws = static_cast<uint8_t *>(workspace);
+    const long long rows = (long long)p.N * a.G;
+    if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (use_tc(dtype, rows)) return D == 64 ? launch_tc<64>(c, p, a, s) : launch_tc<128>(c, p, a, s);
+    return AKV_CA(dtype, D, row_tiles(dtype, rows), launch_ca, c, p, a, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -502,37 +533,31 @@ atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *c, int32_t dtyp
 atlaskv_status atlaskv_cache_attend(atlaskv_cache *c, const atlaskv_seqs *seqs, const atlaskv_cache_attend_io *io,
                                     void *workspace, size_t workspace_bytes, void *stream)
 {
-    AKV_RET(check_cache(c));
     if (!io) return fail(ATLASKV_EINVAL, "null io");
-    akv::CacheParams p;
-    AKV_RET(cache_params(c, seqs, &p));
-    size_t need = 0;
-    AKV_RET(atlaskv_cache_workspace_size(c, io->dtype, seqs->B, seqs->N, io->H, &need));
-    if (!(io->scale >= 0.f) || std::isinf(io->scale)) return fail(ATLASKV_EINVAL, "scale must be finite and >= 0");
-    if (seqs->B == 0) return ATLASKV_OK;
-    const int D = c->d.head_dim;
     akv::CacheAttendIo a = {};
-    int64_t qs;
-    AKV_RET(check_rows("q", io->q, (int64_t)io->H * D, io->dtype, io->q_stride, &qs));
-    if (!io->out || !aligned16(io->out)) return fail(ATLASKV_EINVAL, "null or unaligned out");
-    if (io->lse && !aligned4(io->lse)) return fail(ATLASKV_EINVAL, "unaligned lse");
-    if (need > 0 && (!workspace || ((uintptr_t)workspace & 255u)))
-        return fail(ATLASKV_EINVAL, "workspace must be 256-byte aligned");
-    if (workspace_bytes < need)
-        return fail(ATLASKV_ENOMEM, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     a.q = io->q;
+    a.qs = io->q_stride;
     a.out = io->out;
     a.lse = io->lse;
-    a.qs = qs;
-    a.H = io->H;
-    a.G = io->H / p.H_kv;
-    a.scale_log2 = (io->scale > 0.f ? io->scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-    a.ws = static_cast<uint8_t *>(workspace);
-    const long long rows = (long long)p.N * a.G;
-    if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (use_tc(io->dtype, rows)) return D == 64 ? launch_tc<64>(c, p, a, s) : launch_tc<128>(c, p, a, s);
-    return AKV_CA(io->dtype, D, row_tiles(io->dtype, rows), launch_ca, c, p, a, s);
+    return attend_cache(c, seqs, io->dtype, io->H, io->scale, a, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
+
+atlaskv_status akv_cache_matches(const atlaskv_cache *c, int n_kv_heads, int head_dim)
+{
+    if (c->d.n_kv_heads != n_kv_heads || c->d.head_dim != head_dim)
+        return fail(ATLASKV_EINVAL, "the cache has %d KV heads of %d channels, the tree %d of %d", c->d.n_kv_heads,
+                    c->d.head_dim, n_kv_heads, head_dim);
+    return check_cache(c);
+}
+
+atlaskv_status akv_cache_part(atlaskv_cache *c, const atlaskv_seqs *seqs, int dtype, int H, const void *q, float scale,
+                              float *oseq, float *lse_seq, void *workspace, size_t workspace_bytes, void *stream)
+{
+    akv::CacheAttendIo a = {};
+    a.q = q;
+    a.oseq = oseq;
+    a.lse_seq = lse_seq;
+    return attend_cache(c, seqs, dtype, H, scale, a, workspace, workspace_bytes, stream);
+}

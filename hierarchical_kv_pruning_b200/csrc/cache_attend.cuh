@@ -10,6 +10,8 @@ struct CacheAttendIo {
     const void *q;
     void *out;          // [B][N][H][D]
     float *lse;         // [B][N][H], or null
+    float *oseq;        // not null: the result goes here and to lse_seq, float32, row (b, KV head, g N + n)
+    float *lse_seq;
     long long qs;       // token stride of q in elements
     int H, G;
     float scale_log2;   // scale * log2(e)
@@ -24,6 +26,12 @@ __device__ __forceinline__ void ca_write(const CacheParams &c, const CacheAttend
     const int n = row / io.G, g = row - n * io.G;
     const size_t at = ((size_t)b * c.N + n) * io.H + hkv * io.G + g;
     const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;   // nothing visible: 0; NaN stays
+    if (io.oseq) {
+        const size_t r = (((size_t)b * c.H_kv + hkv) * io.G + g) * c.N + n;
+        *reinterpret_cast<float4 *>(io.oseq + r * D + d4) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (d4 == 0) io.lse_seq[r] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+        return;
+    }
     T *dst = reinterpret_cast<T *>(io.out) + at * D + d4;
     if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);

@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             float *slot = reinterpret_cast<float *>(io.ws + gridDim.x * sizeof(CaDesc)) +
                           ((size_t)blockIdx.x * 2 + (cur.k0 > 0 ? 0 : 1)) * SM::kSlot;
             const int sr = grp * kRows + lrow;
+            const size_t part = (((size_t)cur.e.b * c.H_kv + cur.hkv) * io.G + h) * c.N + n;   // row of oseq
 #pragma unroll
             for (int d = 0; d < D; d += 32) {
                 float o[32];
@@ -461,7 +462,16 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                 }
                 if (!row_ok) continue;
                 // position p of 8 holds channel (p >> 1) + 4 (p & 1)
-                if (whole) {
+                if (whole && io.oseq) {
+                    float *dst = io.oseq + part * D + d;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        *reinterpret_cast<float4 *>(dst + i) =
+                            make_float4(o[i] * inv, o[i + 2] * inv, o[i + 4] * inv, o[i + 6] * inv);
+                        *reinterpret_cast<float4 *>(dst + i + 4) =
+                            make_float4(o[i + 1] * inv, o[i + 3] * inv, o[i + 5] * inv, o[i + 7] * inv);
+                    }
+                } else if (whole) {
                     __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(io.out) + at * D + d;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -478,8 +488,11 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                 }
             }
             if (row_ok) {
-                if (whole) {
-                    if (io.lse) io.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+                const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+                if (whole && io.oseq) {
+                    io.lse_seq[part] = lse;
+                } else if (whole) {
+                    if (io.lse) io.lse[at] = lse;
                 } else {
                     slot[kBlockRows * D + sr] = m;
                     slot[kBlockRows * D + kBlockRows + sr] = l;

@@ -499,6 +499,20 @@ atlaskv_status atlaskv_cache_workspace_size(const atlaskv_cache *cache, int32_t 
 atlaskv_status atlaskv_cache_attend(atlaskv_cache *cache, const atlaskv_seqs *seqs, const atlaskv_cache_attend_io *io,
                                     void *workspace, size_t workspace_bytes, void *stream);
 
+/* atlaskv_attend with the sequence in a cache: the same descent and knowledge
+ * part over `tree` (a uniform tree, host-resident levels allowed; EUNSUPPORTED
+ * for CSR trees), the sequence part as atlaskv_cache_attend of io->q_seq over
+ * `cache` (same H_kv, D), merged by the lambda weights.  io->T, k_seq and v_seq
+ * are ignored; seqs has io's B and N and no q_len, and the new tokens have been
+ * appended.  A query whose sequence is empty gets the knowledge part alone.
+ * Device errors are reported by the tree's and by the cache's sync status.
+ * Workspace: atlaskv_workspace_size_cached() bytes, 256-byte aligned. */
+atlaskv_status atlaskv_workspace_size_cached(const atlaskv_tree *tree, const atlaskv_params *params,
+                                             const atlaskv_cache *cache, int32_t B, int32_t N, int32_t H, size_t *bytes);
+atlaskv_status atlaskv_attend_cached(atlaskv_tree *tree, const atlaskv_params *params, const atlaskv_io *io,
+                                     atlaskv_cache *cache, const atlaskv_seqs *seqs, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* Release the handle and the small device buffers it owns; the caller's
  * buffers are untouched.  NULL is accepted. */
 atlaskv_status atlaskv_destroy(atlaskv_tree *tree);
