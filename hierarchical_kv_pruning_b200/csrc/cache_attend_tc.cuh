@@ -2,28 +2,28 @@
 // bfloat16 queries on tcgen05.
 //
 // An item is a block of 256 query rows of one KV head (row n G + g: token n,
-// head g of the group), as two tiles of 128; its units are the 128-token key
-// tiles up to the last row's causal limit.  One persistent CTA per SM, 16
+// head g of the group), as two tiles of 128; its units are the 64-token key
+// tiles up to the last row's causal limit.  One persistent CTA per SM, 20
 // warps:
-//   copy warp       the codes of 64 tokens at a time into a three-stage ring
-//                   (bulk copies; a page's blocks of one KV head are contiguous);
-//   4 warps         turn them into bfloat16 K and V tiles in the 128-byte
-//                   swizzled operand layout (two stages each); tokens past the
-//                   sequence become zeros.  Within 8 channels a pair of a
+//   copy warp       the codes of a key tile into a ring (bulk copies; a page's
+//                   blocks of one KV head are contiguous);
+//   8 warps         turn them into bfloat16 K and V tiles in the 128-byte
+//                   swizzled operand layout (three stages each); tokens past
+//                   the sequence become zeros.  Within 8 channels a pair of a
 //                   register is (channel i, i + 4), as the nibbles come out; Q
 //                   is stored in the same order, O is put back in the epilogue;
-//   MMA thread      for each key tile, per row tile: S = Q K^T (M 128, N 128),
-//                   later O += P V with P read from TMEM, where it overlays S.
-//                   P V and the next S of one row tile run under the softmax
-//                   of the other;
+//   2 MMA warps     S = Q K^T (M 128, N 64) of the next key tile for both row
+//                   tiles, and O += P V, P read from TMEM where it overlays S;
 //   2 x 4 warps     softmax, one thread per row: as in the few-rows kernel.
-// TMEM: S / P 2 x 128 and O 2 x D columns.  Shared memory (D = 128): Q 64, K 64,
-// V 64, codes 30 KB.
-// What bounds it: per key tile the tensor cores need 2048 cycles (D = 128), the
-// exponentials 2048 on the MUFU pipe, operand reads and the tile writes about
-// 2400 of shared memory's.  256 rows per tile and N = 128 were chosen for the
-// last: with N = 64 the A operand is read twice as often, and with 128 rows
-// the conversion of the codes would not be shared.
+// TMEM: S / P 2 x 2 x 64 and O 2 x D columns.  Shared memory (D = 128): Q 64, K
+// 48, V 48, codes 40 KB.
+// What bounds it: per key tile and both row tiles the tensor cores need 1024
+// cycles (D = 128), the exponentials 1024 on the MUFU pipe, operand reads and
+// the tile writes about 1400 of shared memory's.  256 rows share a tile's
+// conversion.  S is double buffered, so that a row tile's softmax follows
+// its last one at once; 128-token tiles with one S buffer read 20 % less shared
+// memory, but each softmax then waits for two products (6800 cycles per 128 tokens
+// measured, against the 2 x TILECYCLES of this form).
 //
 // The runs of units per CTA are as in the few-rows kernel, unless whole items
 // balance about as well (a partial of 256 rows costs as much as several tiles).
@@ -40,27 +40,30 @@ namespace ctc {
 
 using namespace tc;
 
-constexpr int kRows = 128, kBlockRows = 256, kKeys = 128, kHalf = 64;
-constexpr int kKV = 2, kRaw = 3;    // stages of the K and V tiles, of the codes
-constexpr int kThreads = 512;
-constexpr int kDequantWarp = 8, kMmaWarp = 12, kCopyWarp = 13;
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;   // 2 x 128 x (168 + 88) = the 512 x 128 of the launch
+constexpr int kRows = 128, kBlockRows = 256, kKeys = 64;
+constexpr int kKV = 3, kRaw = 4;    // stages of the K and V tiles, of the codes
+constexpr int kThreads = 640;
+constexpr int kDequantWarp = 8, kDequantWarps = 8, kSWarp = 16, kCopyWarp = 17, kPvWarp = 18;
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 56;   // 256 x 152 + 384 x 56, within the 640 x 96 of the launch
 constexpr float kRescale = 8.f;     // rescale O when a row's maximum grows by more than 2^8
 // A partial costs about this many units to write, read and join.
-constexpr int kPartialUnits = 6;
+constexpr int kPartialUnits = 12;
 
+// [2] x 2: row tile, parity of its running tile count
 constexpr int kBarRawFull = 0, kBarRawEmpty = kBarRawFull + kRaw, kBarKFull = kBarRawEmpty + kRaw,
               kBarKEmpty = kBarKFull + kKV, kBarVFull = kBarKEmpty + kKV, kBarVEmpty = kBarVFull + kKV,
-              kBarS = kBarVEmpty + kKV, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarQ = kBarO + 2,
-              kBarDrained = kBarQ + 2, kBarEnd = kBarDrained + 2, kNumBars = kBarEnd + 1;
+              kBarS = kBarVEmpty + kKV, kBarP = kBarS + 4, kBarO = kBarP + 4, kBarQ = kBarO + 4,
+              kBarDrained = kBarQ + 2, kBarEnd = kBarDrained + 2, kNumBars = kBarEnd + 2;
 
 template <int D>
 struct Smem {
     static constexpr int kQ = kRows * D * 2, kT = kKeys * D * 2, kR = 4 * Blk<D>::kBytes;
     static constexpr int kOffQ = 0, kOffK = 2 * kQ, kOffV = kOffK + kKV * kT, kOffR = kOffV + kKV * kT,
                          kOffBar = kOffR + kRaw * kR, kOffSlot = kOffBar + kNumBars * 8, kOffSched = kOffSlot + 16, kBytes = kOffSched + 64;
-    static constexpr int kColS = 0, kColO = 2 * kKeys;
+    static constexpr int kColS = 0, kColO = 4 * kKeys;
     static constexpr int kSlot = kBlockRows * (D + 2);   // floats of a partial: O, m, l
+    // at D = 64 a tile has 128 groups of 32 channels: half of the warps convert keys, half values
+    static constexpr int kSideWarps = D == 128 ? kDequantWarps : kDequantWarps / 2;
 };
 
 template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
@@ -101,6 +104,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
         "mov.b64 b, {y, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, {%8, %8, %8, %8}, p;\n\t}\n" ::"r"(d),
         "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc), "n"(StepA), "n"(StepB), "r"(0u));
+}
+
+// One lane of a converged warp.  The products are issued under this and not
+// under a comparison of the lane number: the compiler then takes their
+// operands for uniform and needs 5 instructions a product instead of 12.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n" : "=r"(p));
+    return p != 0;
 }
 
 // f(integral constant 0 .. N - 1)
@@ -199,7 +212,6 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
     using namespace ctc;
     using SM = Smem<D>;
     using B = Blk<D>;
-    constexpr int kBlocks = D / 64;   // 64-channel column blocks of a tile
     extern __shared__ __align__(1024) uint8_t ctc_smem[];
     const uint32_t sb = smem_addr(ctc_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
     // scratch of the share's scan, in the ring before its first copy (static
     // shared memory would move the dynamic base off its 1024-byte alignment)
     long long *s_sum = reinterpret_cast<long long *>(ctc_smem + SM::kOffR);
-    int *s_max = reinterpret_cast<int *>(s_sum + 16), *s_items = s_max + 16;
+    int *s_max = reinterpret_cast<int *>(s_sum + kThreads / 32), *s_items = s_max + kThreads / 32;
     griddep_launch();
     griddep_wait();
     CaDesc *desc = reinterpret_cast<CaDesc *>(io.ws) + blockIdx.x;
@@ -283,13 +295,16 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
     if (tid == 0) {
         fence_async_smem();   // the scratch was plainly written, copies come next
         for (int i = 0; i < kNumBars; ++i) {
-            const bool by4 = (i >= kBarRawEmpty && i < kBarKEmpty) || (i >= kBarVFull && i < kBarVEmpty) ||
-                             (i >= kBarP && i < kBarO) || (i >= kBarQ && i < kBarEnd);
-            mbar_init(bar(i), by4 ? 4 : 1);
+            const auto in = [&](int from, int n) { return i >= from && i < from + n; };
+            int count = 1;
+            if (in(kBarRawEmpty, kRaw)) count = kDequantWarps;
+            if (in(kBarKFull, kKV) || in(kBarVFull, kKV)) count = SM::kSideWarps;
+            if (in(kBarP, 4) || in(kBarQ, 2) || in(kBarDrained, 2)) count = 4;
+            mbar_init(bar(i), count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) {
+    if (warp == kSWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
         regs_up<kSoftmaxRegs>();
         const int grp = warp >> 2, lrow = tid & 127, w4 = warp & 3;
         const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
-        const uint32_t tS = tmem + SM::kColS + grp * kKeys + lane_off, tO = tmem + SM::kColO + grp * D + lane_off;
+        const uint32_t tS0 = tmem + SM::kColS + 2 * grp * kKeys + lane_off, tO = tmem + SM::kColO + grp * D + lane_off;
         uint8_t *q_tile = ctc_smem + SM::kOffQ + grp * SM::kQ;
         bool failed = false;
         auto next_own = [&](Seg &x) -> bool {
@@ -337,7 +352,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarQ + grp));
         };
-        int T = 0, seg = 0;   // this group's tiles and stretches so far
+        int T = 0;   // this group's tiles so far
         bool more = next_own(g);
         if (more) load_q(g);
         bool first_seg = true;
@@ -350,36 +365,30 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             const int lim_first = cur.e.s.kv - cur.e.s.q + (cur.e.rb * kBlockRows + grp * kRows) / io.G;
             const bool all_rows = cur.e.rows >= (grp + 1) * kRows;
             float m = -INFINITY, l = 0.f;
+#pragma unroll 1
             for (int t = 0; t < cur.cnt; ++t, ++T) {
-                failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarS + grp), T & 1));
+                const int bs = T & 1;
+                const uint32_t tS = tS0 + bs * kKeys;
+                failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarS + 2 * grp + bs), (T >> 1) & 1));
                 if (failed) break;
                 fence_after_sync();
-                // Two halves of 64 keys: the second is read for its maximum here and again for its
-                // probabilities below (128 logits would not fit the registers).
                 const int key0 = (cur.k0 + t) * kKeys;
-                const bool edge = !all_rows || key0 + kKeys - 1 > lim_first;   // warp-uniform
-                const int hi = lim - key0;
-                float sc[kHalf];
-                auto load_s = [&](int from) {
-                    tmem_ld32(tS + from, sc);
-                    tmem_ld32(tS + from + 32, sc + 32);
-                    tmem_wait_ld();
-                    if (edge) {
+                float sc[kKeys];
+                tmem_ld32(tS, sc);
+                tmem_ld32(tS + 32, sc + 32);
+                tmem_wait_ld();
+                if (!all_rows || key0 + kKeys - 1 > lim_first) {   // warp-uniform
+                    const int hi = lim - key0;
 #pragma unroll
-                        for (int j = 0; j < kHalf; ++j) sc[j] = from + j <= hi ? sc[j] : -INFINITY;
-                    }
-                };
+                    for (int j = 0; j < kKeys; ++j) sc[j] = j <= hi ? sc[j] : -INFINITY;
+                }
                 float mx[8];
-                load_s(kHalf);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) mx[j] = max3(sc[j], sc[j + 8], sc[j + 16]);
 #pragma unroll
                 for (int j = 24; j < 56; j += 2) mx[(j >> 1) & 7] = max3(mx[(j >> 1) & 7], sc[j], sc[j + 1]);
 #pragma unroll
-                for (int j = 56; j < kHalf; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
-                load_s(0);
-#pragma unroll
-                for (int j = 0; j < kHalf; j += 2) mx[(j >> 1) & 7] = max3(mx[(j >> 1) & 7], sc[j], sc[j + 1]);
+                for (int j = 56; j < kKeys; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
                 const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
                 const float m_new = fmaxf(m, top * io.scale_log2);
@@ -387,7 +396,12 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                     m = m_new;
                 } else {
                     const bool need = m_new > m + kRescale;
-                    if (__any_sync(0xffffffffu, need)) {   // the previous P V landed before this S
+                    if (__any_sync(0xffffffffu, need)) {
+                        // O may be rescaled only once the previous P V has landed in it
+                        failed = __any_sync(0xffffffffu,
+                                            !mbar_wait(bar(kBarO + 2 * grp + ((T - 1) & 1)), ((T - 1) >> 1) & 1));
+                        if (failed) break;
+                        fence_after_sync();
                         const float f = need ? fast_exp2(m - m_new) : 1.f;
 #pragma unroll
                         for (int d = 0; d < D; d += 32) {
@@ -411,34 +425,30 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                 for (int j = 0; j < 4; ++j) ps[j] = make_float2(0.f, 0.f);
                 const float2 sc2 = make_float2(io.scale_log2, io.scale_log2), neg2 = make_float2(neg, neg);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half == 1) load_s(kHalf);   // P so far lies over keys 0 .. 31 of S
+                for (int k = 0; k < kKeys; k += 32) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < kHalf; k += 32) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float2 x = fma2(make_float2(sc[k + j], sc[k + j + 1]), sc2, neg2);
-                            x.x = fast_exp2(x.x);
-                            x.y = fast_exp2(x.y);
-                            ps[(j >> 1) & 3] = add2(ps[(j >> 1) & 3], x);
-                            pk[j / 2] = pack_bf16(x.x, x.y);
-                        }
-                        tmem_st16(tS + (half * kHalf + k) / 2, pk);
+                    for (int j = 0; j < 32; j += 2) {
+                        float2 x = fma2(make_float2(sc[k + j], sc[k + j + 1]), sc2, neg2);
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        ps[(j >> 1) & 3] = add2(ps[(j >> 1) & 3], x);
+                        pk[j / 2] = pack_bf16(x.x, x.y);
                     }
+                    tmem_st16(tS + k / 2, pk);
                 }
                 const float2 pt = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
                 l += pt.x + pt.y;
                 tmem_wait_st();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarP + grp));
+                if (lane == 0) mbar_arrive(bar(kBarP + 2 * grp + bs));
             }
             if (failed) break;
             // the stretch's last S is done: Q is free
             more = next_own(g);
             if (more) load_q(g);
-            failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarO + grp), seg & 1));   // the last P V landed
+            failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarO + 2 * grp + ((T - 1) & 1)), ((T - 1) >> 1) & 1));
             if (failed) break;
             fence_after_sync();
             // ---- out: O / l with its log-sum-exp, or a partial ----
@@ -502,89 +512,97 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             if (grp == 0 && lrow == 0 && first_seg)
                 *desc = CaDesc{sch.total, sch.active, cur.k0, cur.e.units, cur.e.b, cur.hkv, cur.e.rb};
             first_seg = false;
-            ++seg;
         }
         if (failed && lane == 0) set_status(c.status, kDevTimeout);
-    } else if (warp < kMmaWarp) {
+    } else if (warp < kSWarp) {
         // ================= codes to bfloat16 tiles =================
         regs_down<kOtherRegs>();
-        const int t128 = tid - kDequantWarp * 32, key = t128 & 63, col = t128 >> 6;   // token of the half tile; 64-channel half of a row
-            bool failed = false;
+        // One group of 32 channels of a token per thread, keys and values apart.  Keys: the lanes of a quad take a token's
+        // groups, so that a warp reads consecutive 16-byte codes; values: consecutive lanes take consecutive
+        // tokens, whose 8-byte pieces are.  Either way the 16-byte stores of 8 lanes fall into
+        // distinct banks.
+        const int w8 = warp - kDequantWarp;
+        const bool does_k = D == 128 || w8 < 4, does_v = D == 128 || w8 >= 4;
+        const int side = D == 128 ? w8 * 32 + lane : (w8 & 3) * 32 + lane;   // 0 .. 64 kGroups - 1
+        const int k_key = side / B::kGroups, k_gr = side % B::kGroups, v_key = side % kKeys, v_gr = side / kKeys;
+        const int k_src = (k_key >> 4) * B::kBytes, v_src = (v_key >> 4) * B::kBytes, k_tok = k_key & 15, v_tok = v_key & 15;
+        const int k_codes = k_src + B::k_codes(k_tok) + 16 * k_gr, k_pair = k_src + B::k_pair(k_tok, k_gr);
+        const int v_codes = v_src + B::v_codes(v_tok, D == 128 ? 2 * v_gr : 4 * v_gr), v_pair = v_src + B::v_scale(v_tok, v_gr);
+        constexpr int kSlice = 64 * B::kSliceBytes / 8;   // bytes from a slice's piece to the next slice's
+        const int k_dst = (k_gr >> 1) * (kKeys * 128) + k_key * 128, v_dst = (v_gr >> 1) * (kKeys * 128) + v_key * 128;
+        const int k_first = (k_gr >> 1) * 2;   // chunk order: the two 64-channel blocks start two chunks apart
+        bool failed = false;
         int T = 0;
         while (!failed && walk.next(c, io, sch, g)) {
+#pragma unroll 1
             for (int t = 0; t < g.cnt; ++t, ++T) {
-                const int st = T % kKV;
-                const int key0 = (g.k0 + t) * kKeys;
-                // the two halves' stages of the ring
-                const int r0 = (2 * T) % kRaw, r1 = (2 * T + 1) % kRaw;
-                failed = !mbar_wait(bar(kBarRawFull + r0), (2 * T / kRaw) & 1) ||
-                         !mbar_wait(bar(kBarRawFull + r1), ((2 * T + 1) / kRaw) & 1) ||
-                         (T >= kKV && !mbar_wait(bar(kBarKEmpty + st), ((T / kKV) + 1) & 1));
-                failed = __any_sync(0xffffffffu, failed);
-                if (failed) break;
+                const int st = T % kKV, rs = T % kRaw, key0 = (g.k0 + t) * kKeys;
+                const uint8_t *raw = ctc_smem + SM::kOffR + rs * SM::kR;
                 const bool tail = key0 + kKeys > g.e.s.kv;   // tokens past the sequence become zeros
-                // 32 channels (group gr of the row) of token `key` of half h: 4 chunks of 16 bytes
-                auto put = [&](uint8_t *tile, int h, int gr, const uint32_t *w, const Scale2 &s) {
-                    const bool zero = tail && key0 + h * kHalf + key >= g.e.s.kv;
-                    uint8_t *dst = tile + (gr >> 1) * (kKeys * 128) + (h * kHalf + key) * 128;
+                failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarRawFull + rs), (T / kRaw) & 1));
+                if (failed) break;
+                uint4 kc;
+                uint32_t kp, vc[4], vs, vm;
+                if (does_k) {
+                    kc = *reinterpret_cast<const uint4 *>(raw + k_codes);
+                    kp = *reinterpret_cast<const uint32_t *>(raw + k_pair);
+                }
+                if (does_v) {
+                    if constexpr (D == 128) {
+                        const uint2 a = *reinterpret_cast<const uint2 *>(raw + v_codes);
+                        const uint2 e = *reinterpret_cast<const uint2 *>(raw + v_codes + kSlice);
+                        vc[0] = a.x;
+                        vc[1] = a.y;
+                        vc[2] = e.x;
+                        vc[3] = e.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vc[i] = *reinterpret_cast<const uint32_t *>(raw + v_codes + i * kSlice);
+                    }
+                    vs = *reinterpret_cast<const uint16_t *>(raw + v_pair);
+                    vm = *reinterpret_cast<const uint16_t *>(raw + v_pair + 4);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarRawEmpty + rs));   // the codes are in registers
+                if (does_k) {
+                    if (T >= kKV) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarKEmpty + st), ((T / kKV) + 1) & 1));
+                    if (failed) break;
+                    uint8_t *dst = ctc_smem + SM::kOffK + st * SM::kT + k_dst;
+                    const Scale2 s = scale2(prmt(kp, kp, 0x1010), prmt(kp, kp, 0x3232));
+                    const bool zero = tail && key0 + k_key >= g.e.s.kv;
+                    const uint32_t w[4] = {k_first ? kc.z : kc.x, k_first ? kc.w : kc.y, k_first ? kc.x : kc.z,
+                                           k_first ? kc.y : kc.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t o[4];
                         stored8(w[i], s, o);
                         uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
                         if (zero) v = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(dst + ((((gr & 1) * 4 + i) ^ (key & 7)) << 4)) = v;
+                        const int ch = (k_gr & 1) * 4 + ((i + k_first) & 3);
+                        *reinterpret_cast<uint4 *>(dst + ((ch ^ (k_key & 7)) << 4)) = v;
                     }
-                };
-                const int tok = key & 15;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t *blk = ctc_smem + SM::kOffR + (h ? r1 : r0) * SM::kR + (key >> 4) * B::kBytes;
-#pragma unroll
-                    for (int gi = 0; gi < kBlocks; ++gi) {
-                        const int gr = col * kBlocks + gi;
-                        const uint32_t pr = *reinterpret_cast<const uint32_t *>(blk + B::k_pair(tok, gr));
-                        const uint4 a = *reinterpret_cast<const uint4 *>(blk + B::k_codes(tok) + gr * 16);
-                        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-                        put(ctc_smem + SM::kOffK + st * SM::kT, h, gr, w, scale2(prmt(pr, pr, 0x1010), prmt(pr, pr, 0x3232)));
-                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarKFull + st));
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarKFull + st));
-                if (T >= kKV) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarVEmpty + st), ((T / kKV) + 1) & 1));
-                if (failed) break;
+                if (does_v) {
+                    if (T >= kKV) failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarVEmpty + st), ((T / kKV) + 1) & 1));
+                    if (failed) break;
+                    uint8_t *dst = ctc_smem + SM::kOffV + st * SM::kT + v_dst;
+                    const Scale2 s = scale2(vs | vs << 16, vm | vm << 16);
+                    const bool zero = tail && key0 + v_key >= g.e.s.kv;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t *blk = ctc_smem + SM::kOffR + (h ? r1 : r0) * SM::kR + (key >> 4) * B::kBytes;
-#pragma unroll
-                    for (int gi = 0; gi < kBlocks; ++gi) {
-                        const int gr = col * kBlocks + gi;
-                        const uint8_t *p = blk + B::v_scale(tok, gr);
-                        const uint32_t s1 = *reinterpret_cast<const uint16_t *>(p);
-                        const uint32_t m1 = *reinterpret_cast<const uint16_t *>(p + 4);
-                        uint32_t w[4];
-                        if constexpr (D == 128) {
-                            const uint2 a = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr));
-                            const uint2 e = *reinterpret_cast<const uint2 *>(blk + B::v_codes(tok, 2 * gr + 1));
-                            w[0] = a.x;
-                            w[1] = a.y;
-                            w[2] = e.x;
-                            w[3] = e.y;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = *reinterpret_cast<const uint32_t *>(blk + B::v_codes(tok, 4 * gr + i));
-                        }
-                        put(ctc_smem + SM::kOffV + st * SM::kT, h, gr, w, scale2(s1 | s1 << 16, m1 | m1 << 16));
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o[4];
+                        stored8(vc[i], s, o);
+                        uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (zero) v = make_uint4(0u, 0u, 0u, 0u);
+                        const int ch = (v_gr & 1) * 4 + i;
+                        *reinterpret_cast<uint4 *>(dst + ((ch ^ (v_key & 7)) << 4)) = v;
                     }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(kBarVFull + st));
-                    mbar_arrive(bar(kBarRawEmpty + r0));
-                    mbar_arrive(bar(kBarRawEmpty + r1));
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarVFull + st));
                 }
             }
         }
@@ -598,8 +616,9 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             const int pshift = 31 - __clz(c.page_size);
             while (!failed && walk.next(c, io, sch, g)) {
                 const int32_t *tab = c.table + (size_t)g.e.b * c.max_pages;
-                for (int i = 0; i < 2 * g.cnt; ++i, ++raw) {
-                    const int rs = raw % kRaw, key = g.k0 * kKeys + i * kHalf;
+#pragma unroll 1
+                for (int i = 0; i < g.cnt; ++i, ++raw) {
+                    const int rs = raw % kRaw, key = (g.k0 + i) * kKeys;
                     const int blocks = max(0, min(4, (g.e.s.kv - key + 15) >> 4));
                     // lane j: the block of tokens key + 16 j
                     const uint8_t *src = nullptr;
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                     }
                     __syncwarp();
                     const uint32_t dst = sb + SM::kOffR + rs * SM::kR;
-                    if (c.page_size >= kHalf) {   // 64 tokens of a page are contiguous
+                    if (c.page_size >= kKeys) {   // 64 tokens of a page are contiguous
                         if (lane == 0 && blocks > 0) bulk_load(dst, src, blocks * B::kBytes, bar(kBarRawFull + rs));
                     } else if (lane < blocks) {
                         bulk_load(dst + lane * B::kBytes, src, B::kBytes, bar(kBarRawFull + rs));
@@ -627,83 +646,96 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             bool landed = true;
             for (int x = max(0, raw - kRaw); x < raw; ++x) landed &= mbar_wait(bar(kBarRawFull + x % kRaw), (x / kRaw) & 1);
             if ((failed || !landed) && lane == 0) set_status(c.status, kDevTimeout);
-        } else if (warp == kMmaWarp && lane == 0) {
-            // ================= MMA issue: one thread =================
-            const uint32_t idesc_s = make_idesc(kRows, kKeys, 0, 0), idesc_o = make_idesc(kRows, D, 0, 1);
-            const uint64_t dq = make_desc(sb + SM::kOffQ, 16, 1024), dk = make_desc(sb + SM::kOffK, 16, 1024),
-                           dv = make_desc(sb + SM::kOffV, kKeys * 128, 1024);
-            const uint32_t hi = (uint32_t)(dq >> 32);   // the same of all three
-            const uint32_t dq0 = (uint32_t)dq, dk0 = (uint32_t)dk, dv0 = (uint32_t)dv;
-            struct Tile {
-                int T, t, cnt;      // running count; index in its stretch and the stretch's tiles
-                bool two;           // both row tiles have rows
-            };
-            int Tg[2] = {0, 0}, Sg[2] = {0, 0};   // tiles (P phases) and stretches (Q loads) of each group so far
-            bool ok = true;
-            auto issue_s = [&](const Tile &x, int grp) -> bool {
-                if (grp == 0 && !mbar_wait(bar(kBarKFull + x.T % kKV), (x.T / kKV) & 1)) return false;
-                if (x.t == 0) {
-                    if (!mbar_wait(bar(kBarQ + grp), Sg[grp] & 1)) return false;
-                    ++Sg[grp];
+        } else if (warp == kSWarp || warp == kPvWarp) {
+            // ================= MMA issue: one lane of a converged warp; S and P V by a warp each =================
+            // Such a warp pays its instructions' latency (a loop that does nothing but issue a key tile's 24 products
+            // takes 1900 cycles; one warp that also waits for all their barriers took 3700), so there are two, and the
+            // bookkeeping is kept to counters.
+            auto wait = [&](int b, int parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)); };
+            int st = 0, ph = 0, n0 = 0, n1 = 0, seg0 = 0, seg1 = 0;   // ring stage and phase; key tiles and stretches
+            bool ok = true;                                           // of each row tile so far
+            if (warp == kSWarp) {
+                const uint32_t idesc = make_idesc(kRows, kKeys, 0, 0);
+                const uint64_t dq = make_desc(sb + SM::kOffQ, 16, 1024), dk = make_desc(sb + SM::kOffK, 16, 1024);
+                const uint32_t hi = (uint32_t)(dq >> 32), dq0 = (uint32_t)dq, dk0 = (uint32_t)dk;
+                auto s_of = [&](int grp, int n, bool last) -> bool {   // S of a row tile's n-th key tile
+                    // its buffer holds the P of two tiles before until its P V is done
+                    const int bs = 2 * grp + (n & 1);
+                    if (n >= 2 && !wait(kBarO + bs, ((n - 2) >> 1) & 1)) return false;
+                    const uint32_t d = tmem + SM::kColS + bs * kKeys, q = dq0 + grp * (SM::kQ >> 4), k = dk0 + st * (SM::kT >> 4);
+                    if (elect_one()) {
+                        steps<D / 16>([&](auto i) {
+                            constexpr int x = i, a = ((x >> 2) * (kRows * 128) + (x & 3) * 32) / 16,
+                                          b = ((x >> 2) * (kKeys * 128) + (x & 3) * 32) / 16;
+                            mma_ss<a, b>(d, q, k, hi, idesc, x > 0 ? 1u : 0u);
+                        });
+                        mma_commit(bar(kBarS + bs));
+                        if (last) mma_commit(bar(kBarKEmpty + st));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                while (ok && __any_sync(0xffffffffu, walk.next(c, io, sch, g))) {
+                    const int cnt = g.cnt;
+                    const bool two = g.e.rows > kRows;
+                    ok = wait(kBarQ, seg0 & 1) && (!two || wait(kBarQ + 1, seg1 & 1));
+#pragma unroll 1
+                    for (int r = 0; ok && r < cnt; ++r) {
+                        ok = wait(kBarKFull + st, ph) && s_of(0, n0, !two) && (!two || s_of(1, n1, true));
+                        ++n0;
+                        n1 += two;
+                        if (++st == kKV) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    ++seg0;
+                    seg1 += two;
                 }
-                fence_after_sync();
-                const uint32_t q = dq0 + ((grp * SM::kQ) >> 4), k = dk0 + (((x.T % kKV) * SM::kT) >> 4);
-                const uint32_t td = tmem + SM::kColS + grp * kKeys;
-                steps<D / 16>([&](auto i) {
-                    constexpr int ks = i, a = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
-                                  b = ((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) / 16;
-                    mma_ss<a, b>(td, q, k, hi, idesc_s, ks > 0 ? 1u : 0u);
-                });
-                mma_commit(bar(kBarS + grp));
-                if (grp == 1 || !x.two) mma_commit(bar(kBarKEmpty + x.T % kKV));
-                return true;
-            };
-            auto issue_pv = [&](const Tile &x, int grp) -> bool {
-                if (grp == 0 && !mbar_wait(bar(kBarVFull + x.T % kKV), (x.T / kKV) & 1)) return false;
-                if (!mbar_wait(bar(kBarP + grp), Tg[grp] & 1)) return false;
-                ++Tg[grp];
-                // a stretch's first P V starts O afresh once the previous O has been read out
-                const int sn = Sg[grp] - 1;
-                if (x.t == 0 && sn > 0 && !mbar_wait(bar(kBarDrained + grp), (sn - 1) & 1)) return false;
-                fence_after_sync();
-                const uint32_t v = dv0 + (((x.T % kKV) * SM::kT) >> 4);
-                const uint32_t ta = tmem + SM::kColS + grp * kKeys, td = tmem + SM::kColO + grp * D;
-                steps<kKeys / 16>([&](auto i) {
-                    constexpr int ks = i;
-                    mma_ts<8 * ks, ks * 128>(td, ta, v, hi, idesc_o, (x.t > 0 || ks > 0) ? 1u : 0u);
-                });
-                if (x.t == x.cnt - 1) mma_commit(bar(kBarO + grp));
-                if (grp == 1 || !x.two) mma_commit(bar(kBarVEmpty + x.T % kKV));
-                return true;
-            };
-            Tile cur{0, 0, 0, false};
-            bool have = walk.next(c, io, sch, g);
-            if (have) {
-                cur = Tile{0, 0, g.cnt, g.e.rows > kRows};
-                ok = issue_s(cur, 0) && (!cur.two || issue_s(cur, 1));
-            }
-            while (have && ok) {
-                Tile nx = cur;
-                ++nx.T;
-                bool more = true;
-                if (cur.t + 1 < cur.cnt) {
-                    ++nx.t;
-                } else {
-                    more = walk.next(c, io, sch, g);
-                    nx.t = 0;
-                    nx.cnt = g.cnt;
-                    nx.two = g.e.rows > kRows;
+            } else {
+                const uint32_t idesc = make_idesc(kRows, D, 0, 1);
+                const uint64_t dv = make_desc(sb + SM::kOffV, kKeys * 128, 1024);
+                const uint32_t hi = (uint32_t)(dv >> 32), dv0 = (uint32_t)dv;
+                auto pv_of = [&](int grp, int n, bool first, int seg, bool last) -> bool {   // O += P V of its n-th key tile
+                    const int bs = 2 * grp + (n & 1);
+                    if (!wait(kBarP + bs, (n >> 1) & 1)) return false;
+                    // a stretch's first P V starts O afresh once the previous O has been read out
+                    if (first && seg > 0 && !wait(kBarDrained + grp, (seg - 1) & 1)) return false;
+                    fence_after_sync();
+                    const uint32_t p = tmem + SM::kColS + bs * kKeys, d = tmem + SM::kColO + grp * D, v = dv0 + st * (SM::kT >> 4);
+                    if (elect_one()) {
+                        steps<kKeys / 16>([&](auto i) {
+                            constexpr int x = i;
+                            mma_ts<8 * x, x * 128>(d, p, v, hi, idesc, (!first || x > 0) ? 1u : 0u);
+                        });
+                        mma_commit(bar(kBarO + bs));
+                        if (last) mma_commit(bar(kBarVEmpty + st));
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                while (ok && __any_sync(0xffffffffu, walk.next(c, io, sch, g))) {
+                    const int cnt = g.cnt;
+                    const bool two = g.e.rows > kRows;
+#pragma unroll 1
+                    for (int r = 0; ok && r < cnt; ++r) {
+                        ok = wait(kBarVFull + st, ph) && pv_of(0, n0, r == 0, seg0, !two) &&
+                             (!two || pv_of(1, n1, r == 0, seg1, true));
+                        ++n0;
+                        n1 += two;
+                        if (++st == kKV) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    ++seg0;
+                    seg1 += two;
                 }
-                // P V of a tile before the next S of the same rows, which overwrites that P
-                ok = issue_pv(cur, 0) && (!more || issue_s(nx, 0));
-                if (ok && cur.two) ok = issue_pv(cur, 1);
-                if (ok && more && nx.two) ok = issue_s(nx, 1);
-                cur = nx;
-                have = more;
             }
             // before TMEM is released every MMA must have completed, on the failure path too
-            mma_commit(bar(kBarEnd));
-            if (!mbar_wait(bar(kBarEnd), 0) || !ok) set_status(c.status, kDevTimeout);
+            const int end = kBarEnd + (warp == kSWarp ? 0 : 1);
+            if (elect_one()) mma_commit(bar(end));
+            if (!wait(end, 0) || !ok) set_status(c.status, kDevTimeout);
         }
         __syncwarp();
     }
@@ -711,7 +743,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (warp == kSWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 }  // namespace akv
