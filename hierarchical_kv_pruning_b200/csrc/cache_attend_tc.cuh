@@ -17,13 +17,15 @@
 //   2 x 4 warps     softmax, one thread per row: as in the few-rows kernel.
 // TMEM: S / P 2 x 2 x 64 and O 2 x D columns.  Shared memory (D = 128): Q 64, K
 // 48, V 48, codes 40 KB.
-// What bounds it: per key tile and both row tiles the tensor cores need 1024
-// cycles (D = 128), the exponentials 1024 on the MUFU pipe, operand reads and
-// the tile writes about 1400 of shared memory's.  256 rows share a tile's
-// conversion.  S is double buffered, so that a row tile's softmax follows
-// its last one at once; 128-token tiles with one S buffer read 20 % less shared
-// memory, but each softmax then waits for two products (6800 cycles per 128 tokens
-// measured, against the 2 x TILECYCLES of this form).
+// What bounds it: per key tile and both row tiles (D = 128) the products take
+// 1280 cycles of the tensor cores and, with their commits and the changes
+// between them, 1900 in a loop that does nothing else; the exponentials 1024 of
+// the MUFU pipe; shared memory about 1400.  A tile takes 2500: the warps that
+// issue pay for their waits.  Measured on the way, cycles per 128 tokens: one
+// S buffer of 128 tokens and one issuing warp 6800 (each softmax waits for two
+// products), 64-token tiles with two S buffers and one issuing warp 7400, products
+// issued under elect.sync instead of one lane's branch 6200, S and P V issued by a
+// warp each 5200, the maximum searched only where it must grow 5000.
 //
 // The runs of units per CTA are as in the few-rows kernel, unless whole items
 // balance about as well (a partial of 256 rows costs as much as several tiles).
@@ -45,7 +47,7 @@ constexpr int kKV = 3, kRaw = 4;    // stages of the K and V tiles, of the codes
 constexpr int kThreads = 640;
 constexpr int kDequantWarp = 8, kDequantWarps = 8, kSWarp = 16, kCopyWarp = 17, kPvWarp = 18;
 constexpr int kSoftmaxRegs = 152, kOtherRegs = 56;   // 256 x 152 + 384 x 56, within the 640 x 96 of the launch
-constexpr float kRescale = 8.f;     // rescale O when a row's maximum grows by more than 2^8
+constexpr float kMaxSum = 1024.f;   // a tile's sum of a row's probabilities that calls for a larger maximum
 // A partial costs about this many units to write, read and join.
 constexpr int kPartialUnits = 12;
 
@@ -382,27 +384,50 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kKeys; ++j) sc[j] = j <= hi ? sc[j] : -INFINITY;
                 }
-                float mx[8];
+                // P over the first 32 columns of S, with the maximum as it is; the row's sum of P
+                auto probabilities = [&]() -> float {
+                    float2 ps[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx[j] = max3(sc[j], sc[j + 8], sc[j + 16]);
+                    for (int j = 0; j < 4; ++j) ps[j] = make_float2(0.f, 0.f);
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    const float2 sc2 = make_float2(io.scale_log2, io.scale_log2), neg2 = make_float2(neg, neg);
 #pragma unroll
-                for (int j = 24; j < 56; j += 2) mx[(j >> 1) & 7] = max3(mx[(j >> 1) & 7], sc[j], sc[j + 1]);
+                    for (int k = 0; k < kKeys; k += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                for (int j = 56; j < kKeys; ++j) mx[j & 7] = fmaxf(mx[j & 7], sc[j]);
-                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-                const float m_new = fmaxf(m, top * io.scale_log2);
-                if (t == 0) {
-                    m = m_new;
-                } else {
-                    const bool need = m_new > m + kRescale;
-                    if (__any_sync(0xffffffffu, need)) {
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 x = fma2(make_float2(sc[k + j], sc[k + j + 1]), sc2, neg2);
+                            x.x = fast_exp2(x.x);
+                            x.y = fast_exp2(x.y);
+                            ps[(j >> 1) & 3] = add2(ps[(j >> 1) & 3], x);
+                            pk[j / 2] = pack_bf16(x.x, x.y);
+                        }
+                        tmem_st16(tS + k / 2, pk);
+                    }
+                    const float2 p = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+                    return p.x + p.y;
+                };
+                // The maximum is only looked for in a stretch's first tile and where a row's sum of probabilities shows that
+                // it has become much too small (or that the row sees its first key): any m gives the same O / l,
+                // and 32 comparisons a tile take a fifth of the softmax's time.
+                float psum = 0.f;
+                bool search = t == 0;
+                if (!search) {
+                    psum = probabilities();
+                    search = __any_sync(0xffffffffu, !(psum <= kMaxSum) || (m == -INFINITY && psum > 0.f));
+                }
+                if (search) {   // warp-uniform
+                    float top = sc[0];
+#pragma unroll
+                    for (int j = 1; j < kKeys - 1; j += 2) top = max3(top, sc[j], sc[j + 1]);
+                    const float m_new = fmaxf(m, fmaxf(top, sc[kKeys - 1]) * io.scale_log2);
+                    if (t > 0) {
                         // O may be rescaled only once the previous P V has landed in it
                         failed = __any_sync(0xffffffffu,
                                             !mbar_wait(bar(kBarO + 2 * grp + ((T - 1) & 1)), ((T - 1) >> 1) & 1));
                         if (failed) break;
                         fence_after_sync();
-                        const float f = need ? fast_exp2(m - m_new) : 1.f;
+                        const float f = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
 #pragma unroll
                         for (int d = 0; d < D; d += 32) {
                             float o[32];
@@ -412,33 +437,12 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                             for (int i = 0; i < 32; ++i) o[i] *= f;
                             tmem_st32(tO + d, o);
                         }
-                        tmem_wait_st();
-                        if (need) {
-                            l *= f;
-                            m = m_new;
-                        }
+                        l *= f;
                     }
+                    m = m_new;
+                    psum = probabilities();
                 }
-                const float neg = m == -INFINITY ? 0.f : -m;
-                float2 ps[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) ps[j] = make_float2(0.f, 0.f);
-                const float2 sc2 = make_float2(io.scale_log2, io.scale_log2), neg2 = make_float2(neg, neg);
-#pragma unroll
-                for (int k = 0; k < kKeys; k += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float2 x = fma2(make_float2(sc[k + j], sc[k + j + 1]), sc2, neg2);
-                        x.x = fast_exp2(x.x);
-                        x.y = fast_exp2(x.y);
-                        ps[(j >> 1) & 3] = add2(ps[(j >> 1) & 3], x);
-                        pk[j / 2] = pack_bf16(x.x, x.y);
-                    }
-                    tmem_st16(tS + k / 2, pk);
-                }
-                const float2 pt = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
-                l += pt.x + pt.y;
+                l += psum;
                 tmem_wait_st();
                 fence_before_sync();
                 __syncwarp();
@@ -648,9 +652,8 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             if ((failed || !landed) && lane == 0) set_status(c.status, kDevTimeout);
         } else if (warp == kSWarp || warp == kPvWarp) {
             // ================= MMA issue: one lane of a converged warp; S and P V by a warp each =================
-            // Such a warp pays its instructions' latency (a loop that does nothing but issue a key tile's 24 products
-            // takes 1900 cycles; one warp that also waits for all their barriers took 3700), so there are two, and the
-            // bookkeeping is kept to counters.
+            // Such a warp pays its instructions' latency (one that waited for all the barriers took 3700 cycles a key
+            // tile), so there are two, and the bookkeeping is kept to counters.
             auto wait = [&](int b, int parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)); };
             int st = 0, ph = 0, n0 = 0, n1 = 0, seg0 = 0, seg1 = 0;   // ring stage and phase; key tiles and stretches
             bool ok = true;                                           // of each row tile so far
