@@ -87,8 +87,10 @@ constexpr float kMinScale = 7.888609052210118e-31f;     // 2^-100
 
 // Quantise the lane's 16 channels; the 32-channel group is 2 neighbouring lanes
 // (all lanes of the warp call it).  The codes of channels 0 .. 7 and 8 .. 15 as
-// two words, channel e at bits 4 e.
-__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad)
+// two words, channel e at bits 4 e.  With Doubt, doubt says whether an error of a
+// few float32 roundings in x could change the minimum, the scale or a code.
+template <bool Doubt>
+__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, bool &doubt)
 {
     // 0 x is NaN for an infinity or NaN and 0 else
     float2 z = make_float2(0.f, 0.f);
@@ -114,8 +116,10 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     low = __float2bfloat16_rd(lo);
     const float m = __bfloat162float(low);
-    scale = __float2bfloat16_ru(__fdiv_rn(hi - m, 15.f));
+    const float step = __fdiv_rn(hi - m, 15.f);
+    scale = __float2bfloat16_ru(step);
     const float s = __bfloat162float(scale);
+    doubt = false;
     if (s < kMinScale) {
         scale = __float2bfloat16(0.f);
         return make_uint2(0u, 0u);
@@ -127,17 +131,82 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
     const float2 inv2 = make_float2(inv, inv), ns2 = make_float2(-s, -s), nm2 = make_float2(-m, -m),
                  magic = make_float2(12582912.f, 12582912.f);
     uint32_t w[2] = {0u, 0u};
+    float off = 0.f;   // largest distance of a quotient from its code
 #pragma unroll
     for (int e = 14; e >= 0; e -= 2) {
         const float2 d = add2(make_float2(x[e], x[e + 1]), nm2);
         float2 q = mul2(d, inv2);
-        q = fma2(fma2(ns2, q, d), inv2, q);
-        q = add2(q, magic);
+        const float2 y = fma2(fma2(ns2, q, d), inv2, q);
+        q = add2(y, magic);
+        if constexpr (Doubt) {
+            const float2 away = add2(y, add2(make_float2(-q.x, -q.y), magic));   // exact
+            off = max3(off, fabsf(away.x), fabsf(away.y));
+        }
         // the bits of 1.5 2^23 are taken off at the end, modulo 2^32
         w[e >> 3] = 16u * w[e >> 3] + __float_as_uint(q.y);
         w[e >> 3] = 16u * w[e >> 3] + __float_as_uint(q.x);
     }
+    if constexpr (Doubt) {
+        // numbers a few units of the last place from a bfloat16, quotients a few from the middle of two codes
+        const auto at_bf16 = [](float f) { return ((__float_as_uint(f) + 4u) & 0xffffu) < 8u; };
+        doubt = at_bf16(lo) || at_bf16(step) || off > 0.5f - 0x1p-21f * (1.f + fmaxf(fabsf(lo), fabsf(hi)) * inv);
+    }
     return make_uint2(w[0] - 0x4b400000u * 0x11111111u, w[1] - 0x4b400000u * 0x11111111u);
+}
+
+// Channel ch of a row in float64, rotated or as it is.
+template <typename T>
+__device__ __forceinline__ double rotated64(const RopeParams &p, const T *row, int ch, int pos, bool rotate)
+{
+    const double x = elem_f32(row[ch]);
+    if (!rotate || ch >= p.rot) return x;
+    const int half = p.rot / 2;
+    const bool first = p.interleaved ? ch % 2 == 0 : ch < half;
+    const int pair = p.interleaved ? ch / 2 : first ? ch : ch - half;
+    const double o = elem_f32(row[p.interleaved ? ch ^ 1 : first ? ch + half : ch - half]);
+    double c, s;
+    turn(pos, p.turns[pair], p.amp, c, s);
+    return first ? x * c - o * s : x * c + o * s;
+}
+
+// The groups that float32 leaves in doubt (one in 2000 of rotated or float32
+// rows; bfloat16 rows as they are, none), decided in float64 from the rows
+// themselves, a channel per lane: what is stored does not depend on float32's
+// roundings.  5.3k tokens take 2 us more.  All lanes of a warp call it, with what
+// quantise16 gave them: lane l of a row holds channels 16 l .. 16 l + 15.
+template <typename T>
+__device__ __forceinline__ void settle(const RopeParams &p, bool doubt, const T *row, int l, int pos, bool rotate,
+                                       uint2 &code, __nv_bfloat16 &scale, __nv_bfloat16 &low)
+{
+    const int lane = threadIdx.x & 31;
+    for (unsigned todo = __ballot_sync(0xffffffffu, doubt); todo;) {   // warp-uniform
+        const int owner = (__ffs(todo) - 1) & ~1;                      // the group's first lane
+        todo &= ~(3u << owner);
+        const T *r = reinterpret_cast<const T *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), owner));
+        const int first = 16 * __shfl_sync(0xffffffffu, l, owner), at = __shfl_sync(0xffffffffu, pos, owner);
+        const bool turned = __shfl_sync(0xffffffffu, rotate ? 1 : 0, owner) != 0;
+        const double x = rotated64(p, r, first + lane, at, turned);
+        double lo = x, hi = x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        const __nv_bfloat16 m = __float2bfloat16_rd(__double2float_rd(lo));
+        const double md = __bfloat162float(m);
+        const __nv_bfloat16 s = __float2bfloat16_ru(__double2float_ru((hi - md) / 15.0));
+        const double t = rint((x - md) / (double)__bfloat162float(s));
+        const uint32_t c = (uint32_t)(int)fmin(fmax(t, 0.0), 15.0) << (4 * (lane & 7));
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __reduce_or_sync(0xffffffffu, lane >> 3 == i ? c : 0u);
+        if ((lane & ~1) == owner) {
+            code = lane & 1 ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+            scale = s;
+            low = m;
+        }
+    }
 }
 
 // Codes to numbers, two at a time (bfloat16 pairs).  A nibble alone in the low 8
@@ -310,8 +379,19 @@ __global__ void __launch_bounds__(kTokThreads, 4)
             }
         }
         __nv_bfloat16 scale, low;
-        bool nf = false;
-        const uint2 code = quantise16(x, scale, low, nf);
+        bool nf = false, doubt = false;
+        uint2 code;
+        const bool inexact = sizeof(T) == 4 || (p.on && is_k);   // of this row, in float32
+        if (__any_sync(0xffffffffu, inexact)) {
+            code = quantise16<true>(x, scale, low, nf, doubt);
+            const float big = fmaxf(fabsf(__bfloat162float(low)), __bfloat162float(scale));
+            const T *src = is_k ? reinterpret_cast<const T *>(io.k) + (t0 + tok1) * io.ks + h1 * D
+                                : reinterpret_cast<const T *>(io.v) + (t0 + tok1) * io.vs + (h1 - c.H_kv) * D;
+            settle<T>(p, doubt && ok && inexact && big < 0x1p100f, src, l,   // (a small group: nothing was clamped)
+                      ok && io.pos ? io.pos[t0 + tok1] : slot, p.on && is_k, code, scale, low);
+        } else {
+            code = quantise16<false>(x, scale, low, nf, doubt);
+        }
         if (!ok) continue;
         bad |= nf;
         const int t = slot & 15;

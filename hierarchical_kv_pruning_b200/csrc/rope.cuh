@@ -70,12 +70,10 @@ template <> __device__ __forceinline__ void store8<float>(float *p, const float 
     *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// cos and sin of `t` turns, |t| <= 1/2, times amp, each rounded once to
-// float32: the Taylor series on an eighth of a turn around the nearest quarter
-// (|x| <= pi / 4: the first terms left out are below 4e-13).  float32
-// functions lose another unit in the last place, and a key that is off by that
-// is stored under the neighbouring code more often.
-__device__ __forceinline__ void turn(int pos, double turns, double amp, float &c, float &s)
+// cos and sin of pos * turns turns, times amp, in float64: the Taylor series on an
+// eighth of a turn around the nearest quarter (|x| <= pi / 4: the first terms
+// left out are below 4e-13).
+__device__ __forceinline__ void turn(int pos, double turns, double amp, double &c, double &s)
 {
     double t = (double)pos * turns;
     t -= rint(t);
@@ -94,9 +92,8 @@ __device__ __forceinline__ void turn(int pos, double turns, double amp, float &c
     e = fma(e, y, -0.5);
     const double sn = fma(a * y, x, x) * amp, cs = fma(e, y, 1.0) * amp;
     const int q = (int)quarter & 3;
-    const float fs = (float)sn, fc = (float)cs;
-    c = q == 0 ? fc : q == 1 ? -fs : q == 2 ? -fc : fs;
-    s = q == 0 ? fs : q == 1 ? fc : q == 2 ? -fs : -fc;
+    c = q == 0 ? cs : q == 1 ? -sn : q == 2 ? -cs : sn;
+    s = q == 0 ? sn : q == 1 ? cs : q == 2 ? -sn : -cs;
 }
 
 constexpr int kTokThreads = 256;   // of the kernels below and of the cache's append
@@ -115,10 +112,10 @@ __device__ __forceinline__ void rope_fill(const RopeParams &p, RopeTable &t, int
         // a load through the generic address: as constant-bank reads the lanes' different addresses would take turns
         double turns;
         asm("ld.f64 %0, [%1];" : "=d"(turns) : "l"(p.turns + e));
-        float c, s;
+        double c, s;
         turn(pos(tok), turns, p.amp, c, s);
-        t.c[tok * kRopeMaxPairs + e] = c;
-        t.s[tok * kRopeMaxPairs + e] = sign * s;
+        t.c[tok * kRopeMaxPairs + e] = (float)c;
+        t.s[tok * kRopeMaxPairs + e] = sign * (float)s;
     }
 }
 

@@ -406,10 +406,11 @@ atlaskv_status atlaskv_rope(const atlaskv_rope_spec *spec, const atlaskv_rope_io
  * so that one copy brings a block, and its codes lie as the matrix
  * instructions want them.  The number stored for code c is
  *   bfloat16(minimum + c * scale)      (one rounding, to nearest even).
- * Storing a group of 32 float32 numbers x: minimum = the smallest x rounded
+ * Storing a group of 32 numbers x: minimum = the smallest x rounded
  * down to bfloat16, scale = (largest x - minimum) / 15 rounded up to bfloat16
  * (0 when below 2^-100), c = (x - minimum) / scale rounded to nearest even and
- * clamped to 0 .. 15.  A stored number differs from x by at most scale / 2,
+ * clamped to 0 .. 15, each quotient as in exact arithmetic (of the rotated key in
+ * float64, not of its float32 value).  A stored number differs from x by at most scale / 2,
  * plus its own rounding to bfloat16 (2^-9 of its magnitude).  Numbers above
  * 2^120 in magnitude are stored as 2^120, NaN as 0; a non-finite number also
  * sets EDEVICE in the cache's sticky status, so that one bad token does not

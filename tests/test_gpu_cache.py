@@ -190,6 +190,31 @@ def test_append_rotates_by_slot_or_position(dtype, inter, rot, D):
             assert torch.equal(vo.cpu().flatten(0, 1).to(F64), ref.value(c, s, m))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,inter,rot", [(128, False, 128), (128, True, 128), (128, False, 48), (64, False, 64),
+                                         (64, True, 16), (64, False, 0)])
+def test_stored_bytes_are_the_definitions(dtype, D, inter, rot):
+    """Minimum, scale and codes as in exact arithmetic, whatever float32 makes of the rotation: the bytes are the
+    reference's (whose float64 roundings could differ with a chance of 1e-8 a number)."""
+    H_kv, P, lens = 2, 64, [700, 333]
+    pages = 20
+    pool = ref.Pool(pages, H_kv, D, P, seed=1)
+    table = tables(lens, P, pages, 3)
+    N = max(lens)
+    k, v = normal(11, 2, N, H_kv, D, dtype=dtype) * 3, normal(12, 2, N, H_kv, D, dtype=dtype)
+    spec = Rope(rot, base=500000.0, interleaved=inter, factor=2.0, amplitude=1.2) if rot else None
+    with new_cache(pool) as cache:
+        cache.append(k.cuda(), v.cuda(), table.cuda(), i32(lens), i32(lens), rope=spec)
+        cache.sync_status()
+        for b, n in enumerate(lens):
+            w = k[b, :n].to(F64)
+            w = ref.rotate(w, torch.arange(n), spec) if rot else w
+            for i in range(n):
+                for h in range(H_kv):
+                    pool.write(int(table[b, i // P]), i % P, h, w[i, h], v[b, i, h].to(F64))
+        assert torch.equal(cache.pages.cpu(), pool.bytes())
+
+
 @pytest.mark.parametrize("D,H_kv,P,lens", [(128, 3, 16, [1, 15, 16, 17, 100, 0]), (64, 1, 256, [300, 256, 5]),
                                            (128, 1, 64, [2000]), (64, 5, 32, [33, 64])])
 @pytest.mark.parametrize("dtype", [BF, F32])
