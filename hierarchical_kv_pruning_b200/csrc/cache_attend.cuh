@@ -102,7 +102,11 @@ constexpr int kCaPartialUnits = 20;
 __host__ __device__ __forceinline__ bool ca_whole(long long items, long long ctas, long long longest, long long total,
                                                   int partial_units)
 {
-    return (items + ctas - 1) / ctas * longest <= (total + ctas - 1) / ctas + partial_units;
+    // ceil(items / ctas) longest <= ceil(total / ctas) + partial_units, without 64-bit divisions where they fit 32 bits
+    const bool small = ((items | total | ctas) >> 31) == 0;
+    const long long rounds = small ? (uint32_t)(items + ctas - 1) / (uint32_t)ctas : (items + ctas - 1) / ctas;
+    const long long run = small ? (uint32_t)(total + ctas - 1) / (uint32_t)ctas : (total + ctas - 1) / ctas;
+    return rounds * longest <= run + partial_units;
 }
 
 // What CTA c left for the join: its first item, where in it the CTA began.
@@ -125,7 +129,14 @@ struct CaSeg {
     int b, hkv, rb, k0, cnt, units;   // cnt = 0: no more
 };
 
-__device__ __forceinline__ long long ca_start(long long total, int active, int c) { return total * c / active; }
+// a / b of numbers >= 0: a 64-bit division takes some 100 instructions, and the
+// plans of small calls are a chain of them.
+__device__ __forceinline__ long long ca_div(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+__device__ __forceinline__ long long ca_start(long long total, int active, int c) { return ca_div(total * c, active); }
 
 __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, const uint32_t *b)
 {
@@ -291,7 +302,7 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                 ++w.b;
                 continue;
             }
-            const int item = (int)(w.whole ? w.off : w.off / units);
+            const int item = (int)(w.whole ? w.off : ca_div(w.off, units));
             g.s = s;
             g.b = w.b;
             g.hkv = item / nb;
@@ -729,7 +740,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const Cache
         const int cta = firsts[fi];
         const CaDesc d = descs[cta];
         const long long item = ca_start(d.total, d.active, cta) - d.k0;
-        const int last = (int)(((item + d.units) * d.active - 1) / d.total);   // CTA of the item's last unit
+        const int last = (int)ca_div((item + d.units) * d.active - 1, d.total);   // CTA of the item's last unit
         const int parts = last - cta + 2;
         const Seq s = load_seq(c, d.b);
         auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * kSlot; };

@@ -194,7 +194,7 @@ struct Walk {
                 ++e;
                 continue;
             }
-            g.hkv = (int)(off / g.e.units);
+            g.hkv = (int)ca_div(off, g.e.units);
             g.k0 = (int)(off - (long long)g.hkv * g.e.units);
             g.cnt = (int)min((long long)(g.e.units - g.k0), s.u1 - u);
             u += g.cnt;

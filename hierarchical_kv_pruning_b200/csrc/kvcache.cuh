@@ -262,7 +262,7 @@ struct AppendIo {
 // slots, fill the table and go through the rows.  Most of the bytes are the
 // queries', but the rounding to codes, about 15 instructions a number, takes
 // as long: side by side the one's memory time hides the other's issue slots
-// (the same CTA doing one after the other measured 51 us where this takes 33,
+// (the same CTA doing one after the other measured 51 us where this took 34,
 // 5.3k tokens of 32 + 2 x 8 heads).
 template <typename T, int D>
 __global__ void __launch_bounds__(kTokThreads, 4)
