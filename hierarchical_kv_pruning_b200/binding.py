@@ -529,11 +529,12 @@ class HikvpTree:
         s = _on_device(cache._index, stream, q_kg, q_seq, block_table, kv_len, out, lse, workspace, *kept)
         shape = (B, N, H, D)
         io = atlaskv_io(B, N, H, N, _dense("q_kg", q_kg, shape, self.dtype), _dense("q_seq", q_seq, shape, self.dtype),
-                        None, None, _dense("out", out, shape, self.dtype), _ptr(lse), _ptr(kept[0]), _ptr(kept[1]),
-                        _ptr(kept[2]))
-        atlaskv_attend_cached(self.handle, p, io, cache.handle, cache._seqs(B, N, block_table, kv_len, None),
-                              workspace.data_ptr(), workspace.nbytes, s)
+                        None, None, _dense("out", out, shape, self.dtype),
+                        None if lse is None else _dense("lse", lse, shape[:3], torch.float32),
+                        *[_ints("kept", x, (B, H, int(k))) for x, k in zip(kept, K)])
+        seqs = cache._seqs(B, N, block_table, kv_len, None)
         _used_on(stream, *new)
+        atlaskv_attend_cached(self.handle, p, io, cache.handle, seqs, workspace.data_ptr(), workspace.nbytes, s)
         return {"out": out, "lse": lse, "kept_root": kept[0], "kept_mid": kept[1], "kept_leaf": kept[2],
                 "workspace": workspace}
 
@@ -727,8 +728,13 @@ def _on_device(index: int, stream, *tensors) -> int:
 
 
 def _used_on(stream, *tensors):
-    """Outputs allocated here belong to the current stream; a call on another one uses them there."""
-    if stream is not None:
+    """Tensors allocated here belong to the current stream, whose earlier work may still use their memory: a call on
+    another stream waits for that, and the memory for the call."""
+    if stream is None or not tensors:
+        return
+    current = torch.cuda.current_stream()
+    if stream.cuda_stream != current.cuda_stream:
+        stream.wait_stream(current)
         for t in tensors:
             t.record_stream(stream)
 
@@ -748,19 +754,19 @@ def rope(x, positions, spec: Rope, out=None, backward: bool = False, stream=None
     """Rotate x [B][N][H][D] by positions [B][N] (int32) into out (a new
     tensor by default; x itself for in place).  backward=True is the transpose:
     it turns a gradient of the rotated tensor into that of the tensor."""
-    shape, dtype, given = x.shape, x.dtype, out
+    shape, dtype, new = x.shape, x.dtype, ()
     if len(shape) != 4 or not x.is_cuda:
         raise AtlaskvError(ATLASKV_EINVAL, "x must be a CUDA tensor [B][N][H][D]")
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
+        new = (out,)
     B, N, H, D = shape
     s = _on_device(x.get_device(), stream, positions, out)
     io = atlaskv_rope_io(_dtype_code(dtype), H, D, B * N, x.data_ptr(), _rows("x", x, shape, dtype),
                          _dense("positions", positions, (B, N), torch.int32), out.data_ptr(),
                          _rows("out", out, shape, dtype), 1 if backward else 0)
+    _used_on(stream, *new)
     atlaskv_rope(spec.spec, io, s)
-    if given is None:
-        _used_on(stream, out)
     return out
 
 
@@ -822,10 +828,13 @@ class KvCache:
         """Store the new tokens' k and v [B][N][H_kv][D] (k rotated when rope
         is given, by positions [B][N] or by slot) and rotate the queries
         q [B][N][H][D] into q_out along the way.  Returns q_out (None without q)."""
+        if k.dim() != 4:
+            raise AtlaskvError(ATLASKV_EINVAL, "k must be [B][N][H_kv][D]")
         B, N = k.shape[:2]
-        dtype, given = k.dtype, q_out
+        dtype, new = k.dtype, ()
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            new = (q_out,)
         s = _on_device(self._index, stream, k, v, block_table, kv_len, q_len, positions, q, q_out)
         shape = (B, N, self.n_kv_heads, self.head_dim)
         qp = qo = None
@@ -836,10 +845,9 @@ class KvCache:
             qp, qs, qo = q.data_ptr(), _rows("q", q, q_shape, dtype), _dense("q_out", q_out, q_shape, dtype)
         io = atlaskv_append_io(_dtype_code(dtype), k.data_ptr(), v.data_ptr(), _rows("k", k, shape, dtype),
                                _rows("v", v, shape, dtype), _ints("positions", positions, (B, N)), H, qp, qs, qo)
-        atlaskv_cache_append(self.handle, None if rope is None else rope.spec,
-                             self._seqs(B, N, block_table, kv_len, q_len), io, s)
-        if q is not None and given is None:
-            _used_on(stream, q_out)
+        seqs = self._seqs(B, N, block_table, kv_len, q_len)
+        _used_on(stream, *new)
+        atlaskv_cache_append(self.handle, None if rope is None else rope.spec, seqs, io, s)
         return q_out
 
     def read(self, N: int, block_table, kv_len, q_len=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
@@ -855,12 +863,11 @@ class KvCache:
         if v_out is None:
             v_out = torch.zeros(shape, dtype=dtype, device=self.device)
             new.append(v_out)
-        if stream is not None and new:   # the zeros were written on the current stream
-            stream.wait_stream(torch.cuda.current_stream())
         s = _on_device(self._index, stream, block_table, kv_len, q_len, k_out, v_out)
-        atlaskv_cache_read(self.handle, self._seqs(shape[0], shape[1], block_table, kv_len, q_len), _dtype_code(dtype),
-                           _dense("k_out", k_out, shape, dtype), _dense("v_out", v_out, shape, dtype), s)
-        _used_on(stream, *new)
+        seqs = self._seqs(shape[0], shape[1], block_table, kv_len, q_len)
+        kp, vp = _dense("k_out", k_out, shape, dtype), _dense("v_out", v_out, shape, dtype)
+        _used_on(stream, *new)   # which includes the zeros' writing
+        atlaskv_cache_read(self.handle, seqs, _dtype_code(dtype), kp, vp, s)
         return k_out, v_out
 
     def workspace_size(self, dtype, B: int, N: int, H: int) -> int:
@@ -870,6 +877,8 @@ class KvCache:
                stream=None):
         """Causal attention of q [B][N][H][D] over the stored sequences:
         (out, lse).  Rows past q_len are left as they were."""
+        if q.dim() != 4:
+            raise AtlaskvError(ATLASKV_EINVAL, "q must be [B][N][H][D]")
         B, N, H, _ = q.shape
         shape, dtype, new = (B, N, H, self.head_dim), q.dtype, []
         if out is None:
@@ -887,10 +896,9 @@ class KvCache:
         io = atlaskv_cache_attend_io(code, H, q.data_ptr(), _rows("q", q, shape, dtype),
                                      _dense("out", out, shape, dtype), _dense("lse", lse, (B, N, H), torch.float32),
                                      scale)
-        atlaskv_cache_attend(self.handle, self._seqs(B, N, block_table, kv_len, q_len), io, workspace.data_ptr(),
-                             workspace.nbytes, s)
-        if new:
-            _used_on(stream, *new)
+        seqs = self._seqs(B, N, block_table, kv_len, q_len)
+        _used_on(stream, *new)
+        atlaskv_cache_attend(self.handle, seqs, io, workspace.data_ptr(), workspace.nbytes, s)
         return out, lse
 
     def sync_status(self, stream=None):

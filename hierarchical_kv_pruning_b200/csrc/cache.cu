@@ -347,6 +347,7 @@ atlaskv_status atlaskv_rope(const atlaskv_rope_spec *spec, const atlaskv_rope_io
     AKV_RET(check_dtype(io->dtype));
     AKV_RET(check_head_dim(io->head_dim));
     if (io->H < 1) return fail(ATLASKV_EINVAL, "H = %d < 1", io->H);
+    if (io->H > (1 << 20)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^20 heads");
     if (io->tokens < 0) return fail(ATLASKV_EINVAL, "tokens < 0");
     if (io->backward != 0 && io->backward != 1) return fail(ATLASKV_EINVAL, "backward is 0 or 1");
     akv::RopeParams p;

@@ -87,10 +87,12 @@ constexpr float kMinScale = 7.888609052210118e-31f;     // 2^-100
 
 // Quantise the lane's 16 channels; the 32-channel group is 2 neighbouring lanes
 // (all lanes of the warp call it).  The codes of channels 0 .. 7 and 8 .. 15 as
-// two words, channel e at bits 4 e.  With Doubt, doubt says whether an error of a
-// few float32 roundings in x could change the minimum, the scale or a code.
+// two words, channel e at bits 4 e.  With Doubt, doubt says whether float32's
+// roundings here, or (turned) a few of them in x, could have changed the minimum,
+// the scale or a code.
 template <bool Doubt>
-__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, bool &doubt)
+__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, bool turned,
+                                            bool &doubt)
 {
     // 0 x is NaN for an infinity or NaN and 0 else
     float2 z = make_float2(0.f, 0.f);
@@ -149,7 +151,7 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
     if constexpr (Doubt) {
         // numbers a few units of the last place from a bfloat16, quotients a few from the middle of two codes
         const auto at_bf16 = [](float f) { return ((__float_as_uint(f) + 4u) & 0xffffu) < 8u; };
-        doubt = at_bf16(lo) || at_bf16(step) || off > 0.5f - 0x1p-21f * (1.f + fmaxf(fabsf(lo), fabsf(hi)) * inv);
+        doubt = (turned && at_bf16(lo)) || at_bf16(step) || off > 0.5f - 0x1p-21f * (1.f + fmaxf(fabsf(lo), fabsf(hi)) * inv);
     }
     return make_uint2(w[0] - 0x4b400000u * 0x11111111u, w[1] - 0x4b400000u * 0x11111111u);
 }
@@ -186,7 +188,8 @@ __device__ __forceinline__ void settle(const RopeParams &p, bool doubt, const T 
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), owner));
         const int first = 16 * __shfl_sync(0xffffffffu, l, owner), at = __shfl_sync(0xffffffffu, pos, owner);
         const bool turned = __shfl_sync(0xffffffffu, rotate ? 1 : 0, owner) != 0;
-        const double x = rotated64(p, r, first + lane, at, turned);
+        double x = rotated64(p, r, first + lane, at, turned);
+        x = isnan(x) ? 0.0 : x;
         double lo = x, hi = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -381,16 +384,17 @@ __global__ void __launch_bounds__(kTokThreads, 4)
         __nv_bfloat16 scale, low;
         bool nf = false, doubt = false;
         uint2 code;
-        const bool inexact = sizeof(T) == 4 || (p.on && is_k);   // of this row, in float32
+        const bool turned = p.on && is_k && 32 * (l / 2) < p.rot;   // this lane's group, at least in part
+        const bool inexact = sizeof(T) == 4 || turned;              // in float32
         if (__any_sync(0xffffffffu, inexact)) {
-            code = quantise16<true>(x, scale, low, nf, doubt);
+            code = quantise16<true>(x, scale, low, nf, turned, doubt);
             const float big = fmaxf(fabsf(__bfloat162float(low)), __bfloat162float(scale));
             const T *src = is_k ? reinterpret_cast<const T *>(io.k) + (t0 + tok1) * io.ks + h1 * D
                                 : reinterpret_cast<const T *>(io.v) + (t0 + tok1) * io.vs + (h1 - c.H_kv) * D;
             settle<T>(p, doubt && ok && inexact && big < 0x1p100f, src, l,   // (a small group: nothing was clamped)
                       ok && io.pos ? io.pos[t0 + tok1] : slot, p.on && is_k, code, scale, low);
         } else {
-            code = quantise16<false>(x, scale, low, nf, doubt);
+            code = quantise16<false>(x, scale, low, nf, false, doubt);
         }
         if (!ok) continue;
         bad |= nf;

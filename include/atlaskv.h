@@ -376,7 +376,7 @@ atlaskv_status atlaskv_rope_init(atlaskv_rope_spec *spec, int32_t layout, int32_
 
 typedef struct {
     int32_t dtype;             /* atlaskv_dtype of x and y */
-    int32_t H;                 /* heads per token, >= 1 */
+    int32_t H;                 /* heads per token, 1 .. 2^20 */
     int32_t head_dim;          /* D: 64 or 128 */
     int64_t tokens;            /* >= 0 */
     const void *x;             /* [tokens][H][D], token t at x + t * x_stride elements */

@@ -154,3 +154,9 @@ def test_reference_storing_stays_within_half_a_step():
     a, b = pool.all([2, 0], 40)
     p, q = pool.history([2, 0], 40)
     assert torch.equal(a.nan_to_num(), p.nan_to_num()) and torch.equal(b.nan_to_num(), q.nan_to_num())
+
+
+def test_rope_refuses_more_heads_than_it_counts(lib):
+    spec = binding.Rope(128).spec
+    for H in ((1 << 20) + 1, (1 << 31) - 1):
+        assert lib.atlaskv_rope(ctypes.byref(spec), ctypes.byref(_rope_io(H=H)), None) == binding.ATLASKV_EUNSUPPORTED

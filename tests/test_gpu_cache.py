@@ -518,3 +518,144 @@ def test_prompt_then_decode(dtype):
                 assert bool(((out[b, :ql[b]].cpu().to(F64) - o).abs() <= to).all())
                 assert bool(((lse[b, :ql[b]].cpu().to(F64) - l).abs() <= tl).all())
         cache.sync_status()
+
+
+# ---- calls that share something ---------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,rot", [(BF, 128), (F32, 0)])
+def test_nan_is_stored_as_zero_in_every_group(dtype, rot):
+    """One NaN in each group of 32 numbers, so that groups which float64 has to decide hold one, too."""
+    H_kv, D, P, n = 2, 128, 64, 900
+    pool = ref.Pool(16, H_kv, D, P, seed=1)
+    table = tables([n], P, 16, 3)
+    k, v = normal(21, 1, n, H_kv, D, dtype=dtype) + 2, normal(22, 1, n, H_kv, D, dtype=dtype) - 2
+    k[..., 5::32], v[..., 9::32] = math.nan, math.nan
+    spec = Rope(rot, base=500000.0) if rot else None
+    with new_cache(pool) as cache:
+        cache.append(k.cuda(), v.cuda(), table.cuda(), i32([n]), i32([n]), rope=spec)
+        with pytest.raises(AtlaskvError) as e:
+            cache.sync_status()
+        assert e.value.status == binding.ATLASKV_EDEVICE
+        w = k[0].to(F64)
+        w = (ref.rotate(w, torch.arange(n), spec) if rot else w).nan_to_num(nan=0.0)
+        for i in range(n):
+            for h in range(H_kv):
+                pool.write(int(table[0, i // P]), i % P, h, w[i, h], v[0, i, h].to(F64).nan_to_num(nan=0.0))
+        assert torch.equal(cache.pages.cpu(), pool.bytes())
+
+
+def test_sequences_share_pages():
+    """A common prefix, and a page twice in one table: reading and attending only look at what the table names."""
+    D, H_kv, H, P = 64, 2, 6, 16
+    pool = ref.Pool(8, H_kv, D, P)
+    pool.fill(torch.arange(8), 8 * P, 3)
+    table = torch.tensor([[1, 2, 3, 4], [1, 2, 6, 6], [5, 5, 5, 5]], dtype=torch.int32)
+    lens = [64, 50, 63]
+    for N in (1, 30):
+        q = normal(4, 3, N, H, D, dtype=BF)
+        with new_cache(pool) as cache:
+            out, lse = cache.attend(q.cuda(), table.cuda(), i32(lens))
+            gk, gv = cache.read(64, table.cuda(), i32(lens), i32(lens))
+            cache.sync_status()
+        for b, n in enumerate(lens):
+            k, v = pool.all(table[b], n)
+            assert torch.equal(gk[b, :n].cpu().to(F64), k) and torch.equal(gv[b, :n].cpu().to(F64), v)
+            o, l, mag, big = ref.attend(q[b].to(F64), k, v, N)
+            to, tl = ref.attend_bounds(BF, n, D, o, l, mag, big)
+            assert bool(((out[b].cpu().to(F64) - o).abs() <= to).all())
+            assert bool(((lse[b].cpu().to(F64) - l).abs() <= tl).all())
+
+
+def test_pages_past_four_gigabytes():
+    D, H_kv, H, P, lens = 128, 8, 16, 256, [700, 300]
+    width = KvCache.page_bytes(H_kv, D, P)
+    n_pages = (1 << 32) // width + 40
+    with KvCache.allocate(n_pages, H_kv, D, P) as far, KvCache.allocate(8, H_kv, D, P) as near:
+        far.pages[-8:].zero_()
+        near.pages.zero_()
+        low = torch.arange(8, dtype=torch.int32).view(2, 4)
+        high = low + (n_pages - 8)
+        spec, kv = Rope(128), i32(lens)
+        for N in (700, 1):
+            q, k, v = (normal(s + N, 2, N, h, D, dtype=BF).cuda() for s, h in ((1, H), (2, H_kv), (3, H_kv)))
+            ql = i32([min(n, N) for n in lens])
+            got = []
+            for cache, tab in ((far, high.cuda()), (near, low.cuda())):
+                r = cache.append(k, v, tab, kv, ql, rope=spec, q=q, q_out=torch.zeros_like(q))
+                out, lse = (torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda"))
+                cache.attend(r, tab, kv, ql, out=out, lse=lse)
+                got.append((r, out, lse) + cache.read(N, tab, kv, ql))
+                cache.sync_status()
+            assert all(torch.equal(a, b) for a, b in zip(*got))
+        assert torch.equal(far.pages[-8:][:3], near.pages[:3])
+
+
+def test_two_calls_at_once():
+    """One cache, two streams, a workspace each: decode steps beside a prompt, again and again."""
+    D, H_kv, H, P = 128, 2, 8, 16
+    pool = ref.Pool(200, H_kv, D, P)
+    table = tables([900, 800, 700], P, 200, 1)
+    for b, n in enumerate([900, 800, 700]):
+        pool.fill(table[b], n, b)
+    dt, kv = table.cuda(), i32([900, 800, 700])
+    q1, q2 = normal(1, 3, 1, H, D, dtype=BF).cuda(), normal(2, 3, 300, H, D, dtype=BF).cuda()
+    with new_cache(pool) as cache:
+        want = [cache.attend(q, dt, kv) for q in (q1, q2)] + [cache.read(700, dt, kv)]
+        torch.cuda.synchronize()
+        sides = [torch.cuda.Stream() for _ in range(3)]
+        for _ in range(5):
+            got = []
+            for q, s in zip((q1, q2), sides):
+                got.append(cache.attend(q, dt, kv, stream=s))
+            got.append(cache.read(700, dt, kv, stream=sides[2]))
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for e, f in zip(want, got) for a, b in zip(e, f))
+        cache.sync_status()
+
+
+def test_outputs_on_another_stream_wait_for_their_memory():
+    """Memory that the current stream's work has not let go of yet is not written by a call on another stream first."""
+    D, H_kv, H, P, N = 128, 2, 8, 16, 70
+    pool = ref.Pool(60, H_kv, D, P)
+    table = tables([400, 300], P, 60, 1)
+    pool.fill(table[0], 400, 1)
+    pool.fill(table[1], 300, 2)
+    dt, kv, spec = table.cuda(), i32([400, 300]), Rope(128)
+    q, k, v = (normal(s, 2, N, h, D, dtype=BF).cuda() for s, h in ((1, H), (2, H_kv), (3, H_kv)))
+    pos = i32([[3] * N] * 2)
+    side = torch.cuda.Stream()
+    with new_cache(pool) as cache:
+        calls = {
+            "rope": lambda s: (binding.rope(q, pos, spec, stream=s),),
+            "append": lambda s: (cache.append(k, v, dt, kv, rope=spec, q=q, stream=s),),
+            "attend": lambda s: cache.attend(q, dt, kv, stream=s),
+            "read": lambda s: cache.read(N, dt, kv, stream=s),
+        }
+        for name, call in calls.items():
+            want = [x.clone() for x in call(None)]
+            torch.cuda.synchronize()
+            old = [torch.empty_like(x) for x in want]
+            torch.cuda._sleep(20_000_000)          # about 10 ms, then the old tensors' last use
+            for x in old:
+                x.fill_(7.0)
+            del old, x
+            got = call(side)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got)), name
+        cache.sync_status()
+
+
+def test_queries_rotated_in_place_and_shapes_refused():
+    D, H_kv, H, P, N = 64, 1, 3, 16, 5
+    spec, kv, ql, tab = Rope(32, interleaved=True), i32([9, 5]), i32([5, 2]), i32([[0], [1]])
+    q, k, v = (normal(s, 2, N, h, D, dtype=F32).cuda() for s, h in ((1, H), (2, H_kv), (3, H_kv)))
+    with KvCache.allocate(2, H_kv, D, P) as cache:
+        want = cache.append(k, v, tab, kv, ql, rope=spec, q=q, q_out=q.clone())
+        assert torch.equal(want[1, 2:], q[1, 2:])
+        r = q.clone()
+        assert cache.append(k, v, tab, kv, ql, rope=spec, q=r, q_out=r).data_ptr() == r.data_ptr()
+        assert torch.equal(r, want)
+        for bad in (lambda: cache.append(k[0], v[0], tab, kv), lambda: cache.attend(q[0], tab, kv)):
+            with pytest.raises(AtlaskvError):
+                bad()
+        cache.sync_status()
