@@ -50,9 +50,14 @@ __device__ __forceinline__ void ca_write(const CacheParams &c, const CacheAttend
 // Per row the online softmax keeps a running maximum m, sum l and output O:
 //     S = q k;  p = 2^(S scale log2 e - m);  l += sum p;  O += p v.
 // What bounds it: the codes are read once and every code becomes a bfloat16,
-// exactly the stored number, at 1.6 instructions a pair; with the softmax and
-// the products that is about 0.07 warp instructions a code against 0.625 bytes, so the
-// issue slots are nearer their limit than HBM.
+// exactly the stored number, at 13 instructions a word of 8.  A unit (D = 128,
+// 8 rows) takes 760 warp instructions for 5120 bytes, 270 of them the 8192 codes'
+// and 64 products; at 2.6 issued a cycle the issue slots are nearer their limit
+// than HBM.  64 sequences of 700 .. 8192 tokens, 8 KV heads, one token of 32 heads
+// (374 MB): 97 us, 3.9 TB/s.  Two of 131k .. 262k tokens, one KV head, 32 rows (76 MB):
+// 51 us; there the products of 4 x 8 rows (38 % of the tensor pipe) and 253
+// registers a thread, so two CTAs an SM, bound it.  One sequence of 513 tokens: 10 us,
+// a chain of two launches, the plan, two units and the join.
 //
 // The products run on m16n8k16 with the cache as the 16-row operand, S^T = K
 // Q^T and O^T = V^T P^T: a decode step has few rows, so they take the 8-wide

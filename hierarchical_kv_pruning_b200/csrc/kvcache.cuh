@@ -266,7 +266,8 @@ struct AppendIo {
 // queries', but the rounding to codes, about 15 instructions a number, takes
 // as long: side by side the one's memory time hides the other's issue slots
 // (the same CTA doing one after the other measured 51 us where this took 34,
-// 5.3k tokens of 32 + 2 x 8 heads).
+// 5.3k tokens of 32 + 2 x 8 heads; with settle it takes 37, 2.5 TB/s: the issue
+// slots, 2.5 instructions a cycle, bound it, not HBM).
 template <typename T, int D>
 __global__ void __launch_bounds__(kTokThreads, 4)
     cache_append_kernel(const __grid_constant__ RopeParams p, const CacheParams c, const AppendIo io)
@@ -465,7 +466,8 @@ __device__ __forceinline__ void store16(T *p, const uint32_t *w, bool wide)
 // A warp reads one block (16 slots of a KV head) of a sequence: HBM bounds it,
 // so all of the block's loads are started before the first code is turned into
 // a number, and a lane writes whole 32-byte sectors.  Slots that the call does
-// not read are skipped at the stores.
+// not read are skipped at the stores.  4 histories of 9k .. 16k tokens, 8 KV heads, D = 128, into
+// bfloat16 (300 MB): 50.8 us, 5.9 TB/s, 90 % of a copy's rate.
 constexpr int kReadWarps = 8;
 
 template <typename T, int D>
