@@ -347,6 +347,18 @@ def test_attend_long_and_ragged(dtype, D, H_kv, H, P, N, lens):
     check_attend(dtype, D, H_kv, H, P, N, lens, [min(n, N) for n in lens], seed=9)
 
 
+@pytest.mark.parametrize("dtype,D,B,H_kv,G,N", [
+    (BF, 128, 2, 1, 4, 1), (BF, 128, 25, 8, 1, 1), (BF, 64, 50, 8, 2, 1), (BF, 128, 30, 2, 4, 3), (BF, 128, 40, 4, 4, 3),
+    (BF, 64, 40, 4, 24, 1), (F32, 128, 50, 2, 3, 1), (F32, 64, 160, 1, 7, 2), (F32, 64, 3, 2, 5, 4),
+])
+def test_attend_with_few_and_many_items(dtype, D, B, H_kv, G, N):
+    """Calls whose items get a large CTA each, share an SM by two, or fill it with small CTAs; one long sequence among them."""
+    lens = [N + (53 * i + 7 * D) % 150 for i in range(B)]
+    lens[-1] = 1900
+    check_attend(dtype, D, H_kv, H_kv * G, 32, N, lens, seed=B)
+    check_attend(dtype, D, H_kv, H_kv * G, 16, N, [N + i % 90 for i in range(B)], seed=G)
+
+
 @pytest.mark.parametrize("spread,scale", [(30.0, 0.0), (1.0, 3.0), (0.01, 1e-3)])
 def test_attend_sharp_and_flat(spread, scale):
     """Logits of hundreds (one key takes all), and almost equal ones."""
