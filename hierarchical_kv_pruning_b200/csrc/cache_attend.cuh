@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
 // found at its first cut: the cut before CTA c is one if the item that CTA c
 // begins inside of began in CTA c - 1's run.  The parts lie in the CTAs' slots:
 // slot 1 of CTA c - 1, where the item began, and slot 0 of c, c + 1, ...  Latency
-// bounds it: all cuts are looked at at once, all weights loaded at once, and
-// each warp has several parts of its share in flight.
+// bounds it: all cuts are looked at at once, and a row's parts are loaded at once,
+// by a warp where they are few (items cut once or twice, as most are) and by the
+// block where they are many (one long sequence).
 constexpr int kJoinThreads = 256, kMaxCtas = 2048;
 
 template <typename T, int D, int RB>
@@ -749,7 +750,38 @@ __global__ void __launch_bounds__(kJoinThreads) cache_combine_kernel(const Cache
         const int parts = last - cta + 2;
         const Seq s = load_seq(c, d.b);
         auto part = [&](int p) { return slots + ((size_t)(cta - 1 + p) * 2 + (p == 0 ? 1 : 0)) * kSlot; };
-        for (int rr = blockIdx.y; rr < RB; rr += gridDim.y) {   // block-uniform
+        if (parts <= 32) {   // a warp a row: a lane a part's weight
+            for (int rr = blockIdx.y * W + warp; rr < RB; rr += gridDim.y * W) {
+                const int row = d.rb * RB + rr;
+                if (row >= io.G * s.q) break;
+                const float m = lane < parts ? part(lane)[RB * D + rr] : -INFINITY;
+                const float l = lane < parts ? part(lane)[RB * D + RB + rr] : 0.f;
+                float M = m;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                const float wt = tc::fast_exp2(m - (M == -INFINITY ? 0.f : M));
+                float L = wt * l, acc[4] = {0.f, 0.f, 0.f, 0.f};   // V of them are a lane's channels
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll 4
+                for (int p = 0; p < parts; ++p) {
+                    const float *q = part(p) + rr * D + lane * V, w = __shfl_sync(0xffffffffu, wt, p);
+                    float v[V];
+                    if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(q);
+                    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(q);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+                }
+                if constexpr (V == 2) {   // four channels to the even lanes
+                    acc[2] = __shfl_down_sync(0xffffffffu, acc[0], 1);
+                    acc[3] = __shfl_down_sync(0xffffffffu, acc[1], 1);
+                }
+                if (V == 4 || lane % 2 == 0)
+                    ca_write<T, D>(c, io, d.b, d.hkv, row, lane * V, make_float4(acc[0], acc[1], acc[2], acc[3]), M, L);
+            }
+            continue;
+        }
+        for (int rr = blockIdx.y; rr < RB; rr += gridDim.y) {   // block-uniform; a row at a time
             const int row = d.rb * RB + rr;
             if (row >= io.G * s.q) break;
             float M = -INFINITY, L = 0.f, acc[V];

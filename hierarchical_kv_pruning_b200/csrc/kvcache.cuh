@@ -88,8 +88,8 @@ constexpr float kMinScale = 7.888609052210118e-31f;     // 2^-100
 // Quantise the lane's 16 channels; the 32-channel group is 2 neighbouring lanes
 // (all lanes of the warp call it).  The codes of channels 0 .. 7 and 8 .. 15 as
 // two words, channel e at bits 4 e.  With Doubt, doubt says whether float32's
-// roundings here, or (turned) a few of them in x, could have changed the minimum,
-// the scale or a code.
+// roundings here, or (turned: the lane's channels are rotated) a few of them in
+// x, could have changed the minimum, the scale or a code.
 template <bool Doubt>
 __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, bool turned,
                                             bool &doubt)
@@ -114,6 +114,7 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
             hi = fmaxf(hi, x[e]);
         }
     }
+    const float own = lo;
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     low = __float2bfloat16_rd(lo);
@@ -151,7 +152,7 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
     if constexpr (Doubt) {
         // numbers a few units of the last place from a bfloat16, quotients a few from the middle of two codes
         const auto at_bf16 = [](float f) { return ((__float_as_uint(f) + 4u) & 0xffffu) < 8u; };
-        doubt = (turned && at_bf16(lo)) || at_bf16(step) || off > 0.5f - 0x1p-21f * (1.f + fmaxf(fabsf(lo), fabsf(hi)) * inv);
+        doubt = (turned && at_bf16(lo) && own <= lo + 0x1p-20f * fabsf(lo)) || at_bf16(step) || off > 0.5f - 0x1p-21f * (1.f + fmaxf(fabsf(lo), fabsf(hi)) * inv);
     }
     return make_uint2(w[0] - 0x4b400000u * 0x11111111u, w[1] - 0x4b400000u * 0x11111111u);
 }
@@ -385,10 +386,9 @@ __global__ void __launch_bounds__(kTokThreads, 4)
         __nv_bfloat16 scale, low;
         bool nf = false, doubt = false;
         uint2 code;
-        const bool turned = p.on && is_k && 32 * (l / 2) < p.rot;   // this lane's group, at least in part
-        const bool inexact = sizeof(T) == 4 || turned;              // in float32
+        const bool inexact = sizeof(T) == 4 || (p.on && is_k && 32 * (l / 2) < p.rot);   // the group, in float32
         if (__any_sync(0xffffffffu, inexact)) {
-            code = quantise16<true>(x, scale, low, nf, turned, doubt);
+            code = quantise16<true>(x, scale, low, nf, p.on && is_k && 16 * l < p.rot, doubt);
             const float big = fmaxf(fabsf(__bfloat162float(low)), __bfloat162float(scale));
             const T *src = is_k ? reinterpret_cast<const T *>(io.k) + (t0 + tok1) * io.ks + h1 * D
                                 : reinterpret_cast<const T *>(io.v) + (t0 + tok1) * io.vs + (h1 - c.H_kv) * D;
