@@ -57,7 +57,7 @@ __device__ __forceinline__ void ca_write(const CacheParams &c, const CacheAttend
 // (374 MB): 97 us, 3.9 TB/s.  Two of 131k .. 262k tokens, one KV head, 32 rows (76 MB):
 // 51 us; there the products of 4 x 8 rows (38 % of the tensor pipe) and 253
 // registers a thread, so two CTAs an SM, bound it.  One sequence of 513 tokens: 10 us,
-// a chain of two launches, the plan, two units and the join.
+// a chain of the plan, the table, a copy and five rounds of units (1 us each).
 //
 // The products run on m16n8k16 with the cache as the 16-row operand, S^T = K
 // Q^T and O^T = V^T P^T: a decode step has few rows, so they take the 8-wide
