@@ -691,7 +691,9 @@ def _refuse(name: str, t: torch.Tensor, shape, dtype, what: str):
 
 def _rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
     """Token stride of a token tensor [B][N][heads][D] whose token rows are
-    dense and evenly spaced, as a slice of a wider projection's is (0: dense)."""
+    dense and evenly spaced, as a slice of a wider projection's is (0: dense).
+    Tokens that share memory, as an expanded tensor's do, are refused: the
+    library takes a stride of 0 for a dense tensor."""
     if t.dtype is not dtype or t.shape != shape:
         _refuse(name, t, shape, dtype, "token")
     if t.is_contiguous():
@@ -701,7 +703,8 @@ def _rows(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
         s1 = s0
     if shape[0] * shape[1] == 1:
         s1 = shape[2] * shape[3]
-    if s3 != 1 or (s2 != shape[3] and shape[2] > 1) or (shape[0] > 1 and s0 != shape[1] * s1):
+    if (s3 != 1 or (s2 != shape[3] and shape[2] > 1) or s1 < shape[2] * shape[3] or
+            (shape[0] > 1 and s0 != shape[1] * s1)):
         _refuse(name, t, shape, dtype, "token")
     return s1
 

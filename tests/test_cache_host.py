@@ -160,3 +160,31 @@ def test_rope_refuses_more_heads_than_it_counts(lib):
     spec = binding.Rope(128).spec
     for H in ((1 << 20) + 1, (1 << 31) - 1):
         assert lib.atlaskv_rope(ctypes.byref(spec), ctypes.byref(_rope_io(H=H)), None) == binding.ATLASKV_EUNSUPPORTED
+
+
+ROW_SHAPES = [((1, 1), (8, 1)), ((1, 1), (3, 5)), ((1, 5), (3, 5)), ((3, 1), (3, 5)), ((1, 1), (1, 5))]
+
+
+@pytest.mark.parametrize("have,want", ROW_SHAPES)
+def test_rows_refuses_tokens_that_share_memory(have, want):
+    """The C ABI takes a token stride of 0 for a dense tensor: an expanded one would be read, or written, past its
+    storage.  Its copy is dense, and one token may have any stride."""
+    shape = torch.Size(want + (4, 128))
+    x = torch.zeros(have + (4, 128)).expand(shape)
+    with pytest.raises(binding.AtlaskvError) as e:
+        binding._rows("x", x, shape, torch.float32)
+    assert e.value.status == binding.ATLASKV_EINVAL
+    assert binding._rows("x", x.contiguous(), shape, torch.float32) == 0
+    over = torch.zeros(4096).as_strided(shape, (want[1] * 256, 256, 128, 1))      # rows of 512 elements, 256 apart
+    with pytest.raises(binding.AtlaskvError):
+        binding._rows("x", over, shape, torch.float32)
+
+
+def test_rows_takes_slices_of_wider_rows():
+    wide = torch.zeros(3, 5, 7, 128)
+    assert binding._rows("x", wide[:, :, :4], torch.Size((3, 5, 4, 128)), torch.float32) == 7 * 128
+    assert binding._rows("x", wide[:, :1, 2:3], torch.Size((3, 1, 1, 128)), torch.float32) == 5 * 7 * 128
+    assert binding._rows("x", wide[:1, :, :4], torch.Size((1, 5, 4, 128)), torch.float32) == 7 * 128
+    one = wide[:1, :1, :4].expand(1, 1, 4, 128)
+    assert binding._rows("x", one, torch.Size((1, 1, 4, 128)), torch.float32) in (0, 4 * 128)
+    assert binding._rows("x", wide[:0, :, :4], torch.Size((0, 5, 4, 128)), torch.float32) == 0

@@ -1,0 +1,36 @@
+"""Calls of the rotary-position and cache operators at the edges of what they
+take: tensors that share memory, groups whose roundings are close, batches that
+mix long and short work, refused calls."""
+import pytest
+import torch
+
+from hierarchical_kv_pruning_b200 import binding
+from hierarchical_kv_pruning_b200.binding import AtlaskvError, KvCache, Rope
+from tests import _cache_ref as ref
+from tests.test_gpu_cache import BF, F32, F64, i32, new_cache, normal, tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("have,want", [((1, 1), (4, 1)), ((1, 1), (4, 3)), ((1, 3), (4, 3)), ((4, 1), (4, 3)), ((1, 1), (1, 3))])
+def test_expanded_tensors_are_refused_and_their_copies_taken(have, want):
+    D, H_kv, H, P = 128, 2, 4, 16
+    B, N = want
+    x, k = normal(1, *have, H, D, dtype=BF).cuda(), normal(2, *have, H_kv, D, dtype=BF).cuda()
+    spec, pos = Rope(128), i32([[5] * N] * B)
+    tab, kv = i32([[b] for b in range(B)]), i32([9] * B)
+    ex, ek = x.expand(B, N, H, D), k.expand(B, N, H_kv, D)
+    cx, ck = ex.contiguous(), ek.contiguous()
+    with KvCache.allocate(B, H_kv, D, P) as cache:
+        cache.pages.zero_()
+        for bad in (lambda: binding.rope(ex, pos, spec), lambda: binding.rope(cx, pos, spec, out=torch.empty_like(x).expand_as(cx)),
+                    lambda: cache.append(ek, ck, tab, kv), lambda: cache.append(ck, ek, tab, kv),
+                    lambda: cache.append(ck, ck, tab, kv, q=ex), lambda: cache.attend(ex, tab, kv)):
+            with pytest.raises(AtlaskvError) as e:
+                bad()
+            assert e.value.status == binding.ATLASKV_EINVAL
+        y = binding.rope(cx, pos, spec)
+        assert torch.equal(y, y[:1, :1].expand_as(y))
+        cache.append(ck, ck, tab, kv, q=cx)
+        cache.attend(cx, tab, kv)
+        cache.sync_status()
