@@ -666,6 +666,8 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                     // its buffer holds the P of two tiles before until its P V is done
                     const int bs = 2 * grp + (n & 1);
                     if (n >= 2 && !wait(kBarO + bs, ((n - 2) >> 1) & 1)) return false;
+                    // that product read P, and the softmax S and P, in the columns that this one writes
+                    fence_after_sync();
                     const uint32_t d = tmem + SM::kColS + bs * kKeys, q = dq0 + grp * (SM::kQ >> 4), k = dk0 + st * (SM::kT >> 4);
                     if (elect_one()) {
                         steps<D / 16>([&](auto i) {

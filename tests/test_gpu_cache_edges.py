@@ -7,7 +7,7 @@ import torch
 from hierarchical_kv_pruning_b200 import binding
 from hierarchical_kv_pruning_b200.binding import AtlaskvError, KvCache, Rope
 from tests import _cache_ref as ref
-from tests.test_gpu_cache import BF, F32, F64, i32, new_cache, normal, tables
+from tests.test_gpu_cache import BF, F32, F64, check_attend, i32, new_cache, normal, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -33,4 +33,21 @@ def test_expanded_tensors_are_refused_and_their_copies_taken(have, want):
         assert torch.equal(binding.rope(cx, pos, spec), one.expand_as(cx))
         cache.append(ck, ck, tab, kv, q=cx)
         cache.attend(cx, tab, kv)
+        cache.sync_status()
+
+
+def test_many_key_tiles_again_and_again():
+    """Row blocks of prompts over many key tiles, so that every buffer of the tensor-memory ring is written over many
+    times by the two issuing warps: right, and the same each time."""
+    check_attend(BF, 128, 1, 4, 64, 130, [2900, 700], seed=31)
+    D, H_kv, H, P, n = 128, 2, 8, 64, 6000
+    pool = ref.Pool(n // P + 3, H_kv, D, P)
+    table = torch.arange(n // P + 1, dtype=torch.int32).repeat(2, 1)
+    pool.fill(table[0], n, 3)
+    dt, kv = table.cuda(), i32([n, n - 77])
+    q = normal(5, 2, 400, H, D, dtype=BF).cuda()
+    with new_cache(pool) as cache:
+        first = cache.attend(q, dt, kv)
+        for _ in range(20):
+            assert all(torch.equal(a, b) for a, b in zip(first, cache.attend(q, dt, kv)))
         cache.sync_status()
