@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                         l *= f;
                     }
                     m = m_new;
+                    if (t > 0) tmem_wait_st();   // P is stored over the first attempt's
                     psum = probabilities();
                 }
                 l += psum;

@@ -51,3 +51,24 @@ def test_many_key_tiles_again_and_again():
         for _ in range(20):
             assert all(torch.equal(a, b) for a, b in zip(first, cache.attend(q, dt, kv)))
         cache.sync_status()
+
+
+def test_maxima_that_grow_along_the_sequence():
+    """Keys that grow fourfold every 64 tokens: each key tile of a prompt makes the softmax store its probabilities
+    again with a larger maximum."""
+    D, P, n, N = 128, 64, 640, 140
+    pool = ref.Pool(n // P, 1, D, P)
+    table = torch.arange(n // P, dtype=torch.int32)[None]
+    d = normal(41, D, dtype=BF)
+    k = normal(42, 1, n, 1, D) + d.float() * (4.0 ** (torch.arange(n) // 64 - 6.0))[:, None, None]
+    v = normal(43, 1, n, 1, D, dtype=BF)
+    q = d + normal(44, 1, N, 4, D, dtype=BF) * 0.1
+    with new_cache(pool) as cache:
+        cache.append(k.to(BF).cuda(), v.cuda(), table.cuda(), i32([n]))
+        out, lse = cache.attend(q.cuda(), table.cuda(), i32([n]), scale=0.3)
+        cache.sync_status()
+        kk, vv = (x[0].cpu().to(F64) for x in cache.read(n, table.cuda(), i32([n])))
+    o, l, mag, big = ref.attend(q[0].to(F64), kk, vv, N, 0.3)
+    to, tl = ref.attend_bounds(BF, n, D, o, l, mag, big)
+    assert bool(((out[0].cpu().to(F64) - o).abs() <= to).all())
+    assert bool(((lse[0].cpu().to(F64) - l).abs() <= tl).all())
