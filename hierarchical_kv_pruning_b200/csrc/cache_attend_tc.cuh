@@ -31,7 +31,8 @@
 // The runs of units per CTA are as in the few-rows kernel, unless whole items
 // balance about as well (a partial of 256 rows costs as much as several tiles).
 //
-// Every wait is bounded; one that gives up sets ETIMEOUT in the status word.
+// Every wait is bounded, by a number of tries within which key tiles have to go
+// on; one that gives up sets ETIMEOUT in the status word.
 #pragma once
 
 #include <type_traits>
@@ -145,6 +146,7 @@ struct Seg {
 struct Sched {
     long long total, off0, u0, u1;   // units of the call; start within entry e0; the CTA's units
     int whole_items, active, e0, nb; // whole items round-robin?; CTAs with units; first entry; row blocks per sequence
+    int copied;                      // key tiles asked for so far (the copy warp's count)
 };
 
 __device__ __forceinline__ Entry entry_at(const CacheParams &c, const CacheAttendIo &io, int nb, int e)
@@ -277,6 +279,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             sch.active = active;
             sch.whole_items = whole;
             sch.nb = nb;
+            sch.copied = 0;
         }
         if (!whole) {
             const long long u0 = ca_start(total, active, blockIdx.x);
@@ -328,6 +331,16 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
         const uint32_t tS0 = tmem + SM::kColS + 2 * grp * kKeys + lane_off, tO = tmem + SM::kColO + grp * D + lane_off;
         uint8_t *q_tile = ctc_smem + SM::kOffQ + grp * SM::kQ;
         bool failed = false;
+        // The second group sits out the stretches of up to 128 rows, so its next S may be many tiles away: the wait's
+        // limit begins anew while tiles are being copied, and still ends when they stop.
+        auto wait_s = [&](uint32_t b, int parity) -> bool {
+            for (int seen = -1;;) {
+                if (mbar_wait(b, parity)) return true;
+                const int now = *const_cast<volatile int *>(&sch.copied);
+                if (now == seen) return false;
+                seen = now;
+            }
+        };
         auto next_own = [&](Seg &x) -> bool {
             while (walk.next(c, io, sch, x))
                 if (x.e.rows > grp * kRows) return true;
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
             for (int t = 0; t < cur.cnt; ++t, ++T) {
                 const int bs = T & 1;
                 const uint32_t tS = tS0 + bs * kKeys;
-                failed = __any_sync(0xffffffffu, !mbar_wait(bar(kBarS + 2 * grp + bs), (T >> 1) & 1));
+                failed = __any_sync(0xffffffffu, !wait_s(bar(kBarS + 2 * grp + bs), (T >> 1) & 1));
                 if (failed) break;
                 fence_after_sync();
                 const int key0 = (cur.k0 + t) * kKeys;
@@ -639,6 +652,7 @@ __global__ void __launch_bounds__(ctc::kThreads, 1)
                         if (blocks > 0) mbar_arrive_expect_tx(bar(kBarRawFull + rs), blocks * B::kBytes);
                         else mbar_arrive(bar(kBarRawFull + rs));
                     }
+                    if (lane == 0) *const_cast<volatile int *>(&sch.copied) = raw + 1;
                     __syncwarp();
                     const uint32_t dst = sb + SM::kOffR + rs * SM::kR;
                     if (c.page_size >= kKeys) {   // 64 tokens of a page are contiguous

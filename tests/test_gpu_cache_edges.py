@@ -72,3 +72,24 @@ def test_maxima_that_grow_along_the_sequence():
     to, tl = ref.attend_bounds(BF, n, D, o, l, mag, big)
     assert bool(((out[0].cpu().to(F64) - o).abs() <= to).all())
     assert bool(((lse[0].cpu().to(F64) - l).abs() <= tl).all())
+
+
+def test_decode_rows_before_a_prompt_block():
+    """One call of many single tokens over a long history and one block of 240 rows a KV head: the row tile that the single tokens
+    leave empty waits for the block through all of them."""
+    D, H_kv, H, P, n, B, N = 128, 2, 8, 64, 2048, 601, 60
+    pool = ref.Pool(n // P, H_kv, D, P)
+    table = torch.arange(n // P, dtype=torch.int32).repeat(B, 1)       # every sequence has the same history
+    pool.fill(table[0], n, 3)
+    one, block = normal(51, 1, 1, H, D, dtype=BF), normal(52, 1, N, H, D, dtype=BF)
+    q = torch.zeros(B, N, H, D, dtype=BF)
+    q[:-1, :1], q[-1:] = one, block
+    ql = [1] * (B - 1) + [N]
+    with new_cache(pool) as cache:
+        out, lse = cache.attend(q.cuda(), table.cuda(), i32([n] * B), i32(ql))
+        cache.sync_status()
+    k, v = pool.all(table[0], n)
+    for x, rows, m in ((one, out[:-1, :1], 1), (block, out[-1:], N)):
+        o, l, mag, big = ref.attend(x[0].to(F64), k, v, m)
+        to, _ = ref.attend_bounds(BF, n, D, o, l, mag, big)
+        assert bool(((rows.cpu().to(F64) - o).abs() <= to).all())
