@@ -85,14 +85,42 @@ __device__ __forceinline__ uint8_t *block_at(const CacheParams &c, int page, int
 constexpr float kMaxStored = 1.329227995784916e36f;     // 2^120
 constexpr float kMinScale = 7.888609052210118e-31f;     // 2^-100
 
+// bfloat16 numbers as float32: the largest one not above x, ...
+__device__ __forceinline__ float bf16_floor(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return __uint_as_float((u + (x < 0.f ? 0xffffu : 0u)) & 0xffff0000u);
+}
+// ... and the smallest one not below x / 15 (x >= 0).  The product is below the
+// quotient by 2^-21 of it at most, so what it rounds up to is one step short at
+// most; 15 times a bfloat16 is a float32, which shows it.
+__device__ __forceinline__ float bf16_ceil15(float x)
+{
+    const uint32_t u = (__float_as_uint(x * (0x1.fffff8p-1f / 15.f)) + 0xffffu) & 0xffff0000u;
+    return __uint_as_float(15.f * __uint_as_float(u) < x ? u + 0x10000u : u);
+}
+__device__ __forceinline__ __nv_bfloat16 upper_half(float x) { return __ushort_as_bfloat16(__float_as_uint(x) >> 16); }
+
 // Quantise the lane's 16 channels; the 32-channel group is 2 neighbouring lanes
 // (all lanes of the warp call it).  The codes of channels 0 .. 7 and 8 .. 15 as
-// two words, channel e at bits 4 e.  With Doubt, doubt says whether float32's
-// roundings here, or (turned: the lane's channels are rotated) a few of them in
-// x, could have changed the minimum, the scale or a code.
+// two words, channel e at bits 4 e.  doubt says whether float32's roundings could
+// have changed the minimum, the scale or a code.  The scale of exact x is exact
+// (the range, rounded up, passes 15 times a bfloat16 only if the exact one does).
+// Rounding can then only change a code where x - m has more bits than a float32.
+//   kExact    x are bfloat16: a difference has more bits only if one number is
+//             2^-14 of the other, and decides a code only if the larger alone lies
+//             in the middle of two.
+//   kFloat    x are float32: the distances of the quotients (below 15.1, two
+//             roundings: 2^-19) from the middle of two codes say so.
+//   kRotated  x are rotated, some of the group's (turned: the lane's): err = 6 2^-24
+//             of the group's largest number covers the rotation by float32 cosines and
+//             the sums lo +- err.
+// The latter two need Doubt, whose lanes may be of any kind.
+enum Exactness { kExact, kFloat, kRotated };
+
 template <bool Doubt>
-__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, bool turned,
-                                            bool &doubt)
+__device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, Exactness kind,
+                                            bool turned, bool &doubt)
 {
     // 0 x is NaN for an infinity or NaN and 0 else
     float2 z = make_float2(0.f, 0.f);
@@ -115,14 +143,25 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
         }
     }
     const float own = lo;
+    float err = 0.f;
+    if constexpr (Doubt) {
+        const float most = fmaxf(fabsf(lo), fabsf(hi));
+        const float r = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        err = kind == kRotated ? 0x1.8p-22f * r : 0.f;
+    }
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-    low = __float2bfloat16_rd(lo);
-    const float m = __bfloat162float(low);
-    const float step = __fdiv_rn(hi - m, 15.f);
-    scale = __float2bfloat16_ru(step);
-    const float s = __bfloat162float(scale);
+    const float m = bf16_floor(lo), range = __fsub_ru(hi, m), s = bf16_ceil15(range);
+    low = upper_half(m);
+    scale = upper_half(s);
     doubt = false;
+    if constexpr (Doubt) {
+        // whether the minimum's neighbourhood holds a bfloat16 (an exact minimum, of a lane that is not turned, stands), or
+        // the range's, with what its own rounding added, 15 times one
+        const float e = fmaf(range, 0x1p-22f, err), below = __uint_as_float(__float_as_uint(s) - 0x10000u);
+        doubt = kind == kRotated && ((turned && own <= lo + 2.f * err && bf16_floor(lo - err) != bf16_floor(lo + err)) ||
+                                     15.f * s < range + e || 15.f * below >= range - e);
+    }
     if (s < kMinScale) {
         scale = __float2bfloat16(0.f);
         return make_uint2(0u, 0u);
@@ -149,10 +188,15 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
         w[e >> 3] = 16u * w[e >> 3] + __float_as_uint(q.y);
         w[e >> 3] = 16u * w[e >> 3] + __float_as_uint(q.x);
     }
-    if constexpr (Doubt) {
-        // numbers a few units of the last place from a bfloat16, quotients a few from the middle of two codes
-        const auto at_bf16 = [](float f) { return ((__float_as_uint(f) + 4u) & 0xffffu) < 8u; };
-        doubt = (turned && at_bf16(lo) && own <= lo + 0x1p-20f * fabsf(lo)) || at_bf16(step) || off > 0.5f - 0x1p-21f * (1.f + fmaxf(fabsf(lo), fabsf(hi)) * inv);
+    if (Doubt && kind != kExact) {
+        doubt |= off > 0.5f - 0x1p-19f - err * inv;
+    } else {
+        const float q = -m * inv, zero = fmaf(fmaf(-s, q, -m), inv, q);   // the quotient of a 0, corrected as above
+        doubt = m != 0.f && fabsf(m) < 0x1p-14f * range;
+        if (fabsf(zero - ((zero + 12582912.f) - 12582912.f)) == 0.5f) {   // hardly ever
+#pragma unroll
+            for (int e = 0; e < 16; ++e) doubt |= x[e] != 0.f && fabsf(x[e]) < 0x1p-14f * fabsf(m);
+        }
     }
     return make_uint2(w[0] - 0x4b400000u * 0x11111111u, w[1] - 0x4b400000u * 0x11111111u);
 }
@@ -173,10 +217,11 @@ __device__ __forceinline__ double rotated64(const RopeParams &p, const T *row, i
 }
 
 // The groups that float32 leaves in doubt (one in 2000 of rotated or float32
-// rows; bfloat16 rows as they are, none), decided in float64 from the rows
+// rows, hardly any of bfloat16 rows as they are), decided in float64 from the rows
 // themselves, a channel per lane: what is stored does not depend on float32's
-// roundings.  5.3k tokens take 2 us more.  All lanes of a warp call it, with what
-// quantise16 gave them: lane l of a row holds channels 16 l .. 16 l + 15.
+// roundings, nor on float64's: the scale rounds up at each step, and a tie is broken
+// by what x - m lost.  5.3k tokens take 2 us more.  All lanes of a warp call it, with
+// what quantise16 gave them: lane l of a row holds channels 16 l .. 16 l + 15.
 template <typename T>
 __device__ __forceinline__ void settle(const RopeParams &p, bool doubt, const T *row, int l, int pos, bool rotate,
                                        uint2 &code, __nv_bfloat16 &scale, __nv_bfloat16 &low)
@@ -190,7 +235,7 @@ __device__ __forceinline__ void settle(const RopeParams &p, bool doubt, const T 
         const int first = 16 * __shfl_sync(0xffffffffu, l, owner), at = __shfl_sync(0xffffffffu, pos, owner);
         const bool turned = __shfl_sync(0xffffffffu, rotate ? 1 : 0, owner) != 0;
         double x = rotated64(p, r, first + lane, at, turned);
-        x = isnan(x) ? 0.0 : x;
+        x = isnan(x) ? 0.0 : fmin(fmax(x, -(double)kMaxStored), (double)kMaxStored);
         double lo = x, hi = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -199,8 +244,15 @@ __device__ __forceinline__ void settle(const RopeParams &p, bool doubt, const T 
         }
         const __nv_bfloat16 m = __float2bfloat16_rd(__double2float_rd(lo));
         const double md = __bfloat162float(m);
-        const __nv_bfloat16 s = __float2bfloat16_ru(__double2float_ru((hi - md) / 15.0));
-        const double t = rint((x - md) / (double)__bfloat162float(s));
+        __nv_bfloat16 s = __float2bfloat16_ru(__double2float_ru(__ddiv_ru(__dsub_ru(hi, md), 15.0)));
+        const double d = x - md, back = d - x, lost = (x - (d - back)) - (md + back);   // d + lost = x - md
+        const double y = d / (double)__bfloat162float(s), floor_y = floor(y);
+        double t = rint(y);
+        if (y - floor_y == 0.5 && lost != 0.0) t = lost > 0.0 ? floor_y + 1.0 : floor_y;
+        if (__bfloat162float(s) < kMinScale) {
+            s = __float2bfloat16(0.f);
+            t = 0.0;
+        }
         const uint32_t c = (uint32_t)(int)fmin(fmax(t, 0.0), 15.0) << (4 * (lane & 7));
         uint32_t w[4];
 #pragma unroll
@@ -386,16 +438,15 @@ __global__ void __launch_bounds__(kTokThreads, 4)
         __nv_bfloat16 scale, low;
         bool nf = false, doubt = false;
         uint2 code;
-        const bool inexact = sizeof(T) == 4 || (p.on && is_k && 32 * (l / 2) < p.rot);   // the group, in float32
-        if (__any_sync(0xffffffffu, inexact)) {
-            code = quantise16<true>(x, scale, low, nf, p.on && is_k && 16 * l < p.rot, doubt);
-            const float big = fmaxf(fabsf(__bfloat162float(low)), __bfloat162float(scale));
+        const Exactness kind = p.on && is_k && 32 * (l / 2) < p.rot ? kRotated : sizeof(T) == 4 ? kFloat : kExact;
+        if (__any_sync(0xffffffffu, kind != kExact))
+            code = quantise16<true>(x, scale, low, nf, kind, p.on && is_k && 16 * l < p.rot, doubt);
+        else
+            code = quantise16<false>(x, scale, low, nf, kind, false, doubt);
+        if (__any_sync(0xffffffffu, doubt && ok)) {
             const T *src = is_k ? reinterpret_cast<const T *>(io.k) + (t0 + tok1) * io.ks + h1 * D
                                 : reinterpret_cast<const T *>(io.v) + (t0 + tok1) * io.vs + (h1 - c.H_kv) * D;
-            settle<T>(p, doubt && ok && inexact && big < 0x1p100f, src, l,   // (a small group: nothing was clamped)
-                      ok && io.pos ? io.pos[t0 + tok1] : slot, p.on && is_k, code, scale, low);
-        } else {
-            code = quantise16<false>(x, scale, low, nf, false, doubt);
+            settle<T>(p, doubt && ok, src, l, ok && io.pos ? io.pos[t0 + tok1] : slot, p.on && is_k, code, scale, low);
         }
         if (!ok) continue;
         bad |= nf;

@@ -93,3 +93,120 @@ def test_decode_rows_before_a_prompt_block():
         o, l, mag, big = ref.attend(x[0].to(F64), k, v, m)
         to, _ = ref.attend_bounds(BF, n, D, o, l, mag, big)
         assert bool(((rows.cpu().to(F64) - o).abs() <= to).all())
+
+
+# ---- stored bytes where the roundings are close ---------------------------------------
+
+def stored_bytes(pool, table, lens, k, v):
+    """Fill the pool with the definition's bytes of k, v [B][N][H_kv][D] (float64), all tokens at once."""
+    kc, ks, vc, vs = ref.addresses(pool.D)
+    for b, n in enumerate(lens):
+        slot = torch.arange(n)
+        page, blk, tok = table[b, slot // pool.P].long(), slot % pool.P // 16, slot % 16
+        at = [x.view(-1, 1, 1) for x in (page, blk)]
+        head = torch.arange(pool.H).view(1, -1, 1)
+        for x, code, sc, dl in ((k[b, :n], kc, ks, 2), (v[b, :n], vc, vs, 4)):
+            c, s, m = ref.quantise(x)
+            pool.raw[at[0], head, at[1], code[tok][:, None, ::2]] = (c[..., ::2] | (c[..., 1::2] << 4)).to(torch.uint8)
+            for o, w in ((0, s), (dl, m)):
+                bits = w.contiguous().view(torch.int16).to(torch.int32) & 0xffff
+                where = sc[tok][:, None, ::32] + o
+                pool.raw[at[0], head, at[1], where] = (bits & 255).to(torch.uint8)
+                pool.raw[at[0], head, at[1], where + 1] = (bits >> 8).to(torch.uint8)
+
+
+def check_bytes(k, v, spec, P=64):
+    """What append stores of k, v [1][n][H_kv][D] in slots 0 .. n - 1 against the definition."""
+    n, H_kv, D = k.shape[1:]
+    pool = ref.Pool(-(-n // P), H_kv, D, P, seed=1)
+    table = torch.randperm(-(-n // P), generator=torch.Generator().manual_seed(7)).to(torch.int32)[None]
+    with new_cache(pool) as cache:
+        cache.append(k.cuda(), v.cuda(), table.cuda(), i32([n]), rope=spec)
+        cache.sync_status()
+        got = cache.pages.cpu()
+    w = k.to(F64)
+    w = ref.rotate(w[0], torch.arange(n), spec)[None] if spec else w
+    stored_bytes(pool, table, [n], w, v.to(F64))
+    assert torch.equal(got, pool.bytes()), int((got != pool.bytes()).sum())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,H_kv", [(128, 4), (64, 1)])
+def test_stored_bytes_of_tiny_numbers_beside_large_ones(dtype, D, H_kv):
+    """Groups in which a number is 2^-30 of the range: the difference to the minimum has more bits than a float32, and
+    it decides the scale's rounding (a range just above 15 codes) or which of two codes is nearer (a tie without it)."""
+    tiny = 2.0 ** -30
+    base = torch.linspace(0.25, 14.0, 32).to(BF).float()
+
+    def group(*special):
+        x = base.clone()
+        x[torch.tensor([5 * i + 1 for i in range(len(special))])] = torch.tensor(special)
+        return x
+    groups = [group(15.0, -tiny), group(15.0, tiny), group(15.0, 0.0)]                    # scale 1.0078125, 1, 1
+    step = 0.99609375                                                                     # of a range of 14.9375
+    for low in (-tiny, tiny, 0.0):
+        groups.append(torch.cat([group(14.9375, low, step / 2, step)[:31], torch.tensor([step / 2])]))
+    for h in (0.5, 1.5, 4.5, 7.5):                                                        # scale 1, minimum -h
+        mid = torch.linspace(-h, 15.0 - h, 32).to(BF).float()
+        for t in (tiny, -tiny, 0.0):
+            x = mid.clone()
+            x[0], x[31], x[7], x[20] = -h, 15.0 - h, t, -t
+            groups.append(x)
+    x = torch.stack(groups)
+    x = torch.cat([x * s for s in (1.0, 2.0 ** 40, 2.0 ** -40, 2.0 ** 100)])
+    order = torch.randperm(len(x) * 8, generator=torch.Generator().manual_seed(2))
+    rows = x.repeat(8, 1)[order][: len(x) * 8 // (D // 32 * H_kv) * (D // 32 * H_kv)].view(1, -1, H_kv, D).to(dtype)
+    check_bytes(rows, rows.flip(1), None)
+
+
+def turned_back(target, spec, dtype):
+    """Keys whose rotation by their slots is about target [n][H_kv][D]."""
+    return (ref.rotate(target, torch.arange(target.shape[0]), spec, backward=True) / spec.spec.amplitude ** 2).to(dtype)[None]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,inter,rot", [(128, False, 128), (128, True, 128), (128, False, 48), (64, False, 64),
+                                         (128, False, 96), (64, True, 48), (64, False, 16)])
+@pytest.mark.parametrize("kind", ["offsets", "narrow"])
+def test_stored_bytes_of_rotations_that_cancel(dtype, D, inter, rot, kind):
+    """Keys with channel offsets, and groups whose range is small beside their offset."""
+    H_kv, n = 2, 1500
+    spec = Rope(rot, base=500000.0, interleaved=inter, factor=2.0, amplitude=1.2)
+    g = torch.Generator().manual_seed(61)
+    x = torch.randn(n, H_kv, D, generator=g, dtype=F64)
+    if kind == "offsets":
+        x += 4 * torch.randn(H_kv, D, generator=g, dtype=F64)
+    else:
+        x = 100 + 0.5 * x
+    k = turned_back(x, spec, dtype)
+    check_bytes(k, normal(62, 1, n, H_kv, D, dtype=dtype), spec)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_stored_bytes_of_huge_and_tiny_groups(dtype):
+    """Rotated groups above 2^100, where they used not to be decided in float64, and around the smallest scale."""
+    spec = Rope(128, amplitude=0.9)
+    x = torch.randn(800, 1, 128, generator=torch.Generator().manual_seed(63), dtype=F64)
+    e = torch.arange(800) % 8
+    x *= (2.0 ** torch.tensor([110.0, 117.0, 101.0, 0.0, -98.0, -99.0, -100.0, -104.0], dtype=F64))[e][:, None, None]
+    k = turned_back(x, spec, dtype)
+    n = k.shape[1]
+    w = ref.rotate(k[0].to(F64), torch.arange(n), spec)
+    assert float(w.abs().max()) < 2.0 ** 120
+    pool = ref.Pool(16, 1, 128, 64, seed=1)
+    table = torch.arange(16, dtype=torch.int32)[None]
+    with new_cache(pool) as cache:
+        cache.append(k.cuda(), k.cuda(), table.cuda(), i32([n]), rope=spec)
+        cache.sync_status()
+        got = cache.pages.cpu()
+    want = ref.Pool(16, 1, 128, 64, seed=1)
+    stored_bytes(want, table, [n], w[None], k.to(F64))
+    # groups whose scale is below 2^-100 have scale 0 and codes 0
+    kc, ks, vc, vs = ref.addresses(128)
+    for y, code, sc in ((w, kc, ks), (k[0].to(F64), vc, vs)):
+        s = ref.quantise(y)[1]
+        for t, _, gr in torch.nonzero(s.to(F64) < 2.0 ** -100).tolist():
+            blk = want.raw[t // 64, 0, t % 64 // 16]
+            blk[code[t % 16, 32 * gr:32 * gr + 32:2]] = 0
+            blk[sc[t % 16, 32 * gr]] = blk[sc[t % 16, 32 * gr] + 1] = 0
+    assert torch.equal(got, want.bytes()), int((got != want.bytes()).sum())
