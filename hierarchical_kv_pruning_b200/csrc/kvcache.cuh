@@ -112,15 +112,17 @@ __device__ __forceinline__ __nv_bfloat16 upper_half(float x) { return __ushort_a
 //             in the middle of two.
 //   kFloat    x are float32: the distances of the quotients (below 15.1, two
 //             roundings: 2^-19) from the middle of two codes say so.
-//   kRotated  x are rotated, some of the group's (turned: the lane's): err = 6 2^-24
-//             of the group's largest number covers the rotation by float32 cosines and
-//             the sums lo +- err.
+//   kRotated  x are rotated, some of the group's (turned: the lane's): a rotation
+//             by float32 cosines is off by at most 3.3 2^-24 of the pair's radius,
+//             that is 4.6 2^-24 of the larger of its two results.  pair0 and pair1
+//             are the lanes with the partners of the lane's two chunks; err = 6
+//             2^-24 of the largest result there and here covers the sums lo +- err, too.
 // The latter two need Doubt, whose lanes may be of any kind.
 enum Exactness { kExact, kFloat, kRotated };
 
 template <bool Doubt>
 __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv_bfloat16 &low, bool &bad, Exactness kind,
-                                            bool turned, bool &doubt)
+                                            bool turned, int pair0, int pair1, bool &doubt)
 {
     // 0 x is NaN for an infinity or NaN and 0 else
     float2 z = make_float2(0.f, 0.f);
@@ -146,7 +148,8 @@ __device__ __forceinline__ uint2 quantise16(float *x, __nv_bfloat16 &scale, __nv
     float err = 0.f;
     if constexpr (Doubt) {
         const float most = fmaxf(fabsf(lo), fabsf(hi));
-        const float r = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        float r = max3(most, __shfl_sync(0xffffffffu, most, pair0), __shfl_sync(0xffffffffu, most, pair1));
+        r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 1));
         err = kind == kRotated ? 0x1.8p-22f * r : 0.f;
     }
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
@@ -390,6 +393,9 @@ __global__ void __launch_bounds__(kTokThreads, 4)
     load(tok, h, raw);
     begin();
     const int hc = p.rot / 16;                    // chunks of 8 channels in a half
+    // half layout: the lanes that hold the partners of this lane's two chunks
+    const auto partner = [&](int ch) { return ch >= 2 * hc || p.interleaved ? ch : ch < hc ? ch + hc : ch - hc; };
+    const int pair0 = row0 + (partner(2 * l) >> 1), pair1 = row0 + (partner(2 * l + 1) >> 1);
     for (int base = 0; base < n * rows; base += R) {   // CTA-uniform
         const int slot = tok < n ? s_slot[tok] : -1;
         const bool is_k = slot >= 0 && h < c.H_kv, ok = slot >= 0;
@@ -409,10 +415,9 @@ __global__ void __launch_bounds__(kTokThreads, 4)
                 float o[16];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int ch = 2 * l + k, pc = ch >= 2 * hc ? ch : ch < hc ? ch + hc : ch - hc;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        o[8 * k + e] = __shfl_sync(0xffffffffu, swap ? x[8 * (1 - k) + e] : x[8 * k + e], row0 + (pc >> 1));
+                        o[8 * k + e] = __shfl_sync(0xffffffffu, swap ? x[8 * (1 - k) + e] : x[8 * k + e], k ? pair1 : pair0);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -440,9 +445,9 @@ __global__ void __launch_bounds__(kTokThreads, 4)
         uint2 code;
         const Exactness kind = p.on && is_k && 32 * (l / 2) < p.rot ? kRotated : sizeof(T) == 4 ? kFloat : kExact;
         if (__any_sync(0xffffffffu, kind != kExact))
-            code = quantise16<true>(x, scale, low, nf, kind, p.on && is_k && 16 * l < p.rot, doubt);
+            code = quantise16<true>(x, scale, low, nf, kind, p.on && is_k && 16 * l < p.rot, pair0, pair1, doubt);
         else
-            code = quantise16<false>(x, scale, low, nf, kind, false, doubt);
+            code = quantise16<false>(x, scale, low, nf, kind, false, pair0, pair1, doubt);
         if (__any_sync(0xffffffffu, doubt && ok)) {
             const T *src = is_k ? reinterpret_cast<const T *>(io.k) + (t0 + tok1) * io.ks + h1 * D
                                 : reinterpret_cast<const T *>(io.v) + (t0 + tok1) * io.vs + (h1 - c.H_kv) * D;

@@ -167,14 +167,22 @@ def turned_back(target, spec, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("D,inter,rot", [(128, False, 128), (128, True, 128), (128, False, 48), (64, False, 64),
                                          (128, False, 96), (64, True, 48), (64, False, 16)])
-@pytest.mark.parametrize("kind", ["offsets", "narrow"])
+@pytest.mark.parametrize("kind", ["small first half", "small second half", "offsets", "narrow"])
 def test_stored_bytes_of_rotations_that_cancel(dtype, D, inter, rot, kind):
-    """Keys with channel offsets, and groups whose range is small beside their offset."""
+    """Rotated numbers far smaller than their pairs (a group's partners a thousand times as large), keys with channel
+    offsets, and groups whose range is small beside their offset: float32's error is that of the pair."""
     H_kv, n = 2, 1500
     spec = Rope(rot, base=500000.0, interleaved=inter, factor=2.0, amplitude=1.2)
     g = torch.Generator().manual_seed(61)
     x = torch.randn(n, H_kv, D, generator=g, dtype=F64)
-    if kind == "offsets":
+    i = torch.arange(rot // 2)
+    first = 2 * i if inter else i
+    second = first + (1 if inter else rot // 2)
+    if kind == "small first half":
+        x[..., second] *= 1000
+    elif kind == "small second half":
+        x[..., first] *= 1000
+    elif kind == "offsets":
         x += 4 * torch.randn(H_kv, D, generator=g, dtype=F64)
     else:
         x = 100 + 0.5 * x
