@@ -1683,8 +1683,8 @@ atlaskv_status atlaskv_attend_cached(atlaskv_tree *t, const atlaskv_params *p, c
         return fail(ATLASKV_EINVAL, "seqs (B = %d, N = %d) and io (B = %d, N = %d) differ", seqs->B, seqs->N, io->B, io->N);
     if (seqs->q_len) return fail(ATLASKV_EINVAL, "q_len must be NULL: every query has N tokens");
     if (io->B == 0) return ATLASKV_OK;
-    if (!seqs->block_table || !seqs->kv_len || seqs->max_pages < 1)
-        return fail(ATLASKV_EINVAL, "null block_table or kv_len, or max_pages < 1");
+    // all refusals come before the first launch: work in flight on the tree's streams could not be taken back
+    AKV_RET(akv_cache_check(cache, seqs, t->d.dtype, io->H, io->q_seq, p->scale));
     cs.seqs = seqs;
     atlaskv_io x = *io;
     x.T = x.N;                      // no sequence tensors: the knowledge part reads neither of these

@@ -231,6 +231,8 @@ atlaskv_status launch_ca(const atlaskv_cache *c, const akv::CacheParams &p, cons
 // codes into bfloat16 again for every 32 rows).
 bool use_tc(int dtype, long long rows) { return dtype == ATLASKV_BF16 && rows > 32; }
 
+long long tc_blocks(long long rows) { return (rows + akv::ctc::kBlockRows - 1) / akv::ctc::kBlockRows; }
+
 template <int D>
 size_t tc_workspace(const atlaskv_cache *c)
 {
@@ -241,8 +243,7 @@ template <int D>
 atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, const akv::CacheAttendIo &a, cudaStream_t s)
 {
     constexpr int RB = akv::ctc::kBlockRows;
-    const long long nb = ((long long)p.N * a.G + RB - 1) / RB;
-    if (nb * p.B * p.H_kv > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "too many query rows for one call");
+    const long long nb = tc_blocks((long long)p.N * a.G);
     AKV_RET(akv_smem_limit(reinterpret_cast<const void *>(akv::cache_attend_tc_kernel<D>), akv::ctc::Smem<D>::kBytes));
     const int n = c->num_sms;
     AKV_RET(launch_pdl(akv::cache_attend_tc_kernel<D>, dim3(n), akv::ctc::kThreads, akv::ctc::Smem<D>::kBytes, s, p, a,
@@ -277,20 +278,34 @@ atlaskv_status launch_tc(const atlaskv_cache *c, const akv::CacheParams &p, cons
         }                                                                            \
     } while (0)
 
+// What attention over the cache needs of the sequences and of q, without its
+// outputs and workspace.  On OK with B > 0, *qs is q's token stride in elements.
+atlaskv_status check_attend(const atlaskv_cache *c, const atlaskv_seqs *seqs, int dtype, int H, float scale, const void *q,
+                            int64_t q_stride, akv::CacheParams *p, int64_t *qs, size_t *need)
+{
+    AKV_RET(check_cache(c));
+    AKV_RET(cache_params(c, seqs, p));
+    AKV_RET(atlaskv_cache_workspace_size(c, dtype, seqs->B, seqs->N, H, need));
+    if (!(scale >= 0.f) || std::isinf(scale)) return fail(ATLASKV_EINVAL, "scale must be finite and >= 0");
+    if (seqs->B == 0) return ATLASKV_OK;
+    AKV_RET(check_rows("q", q, (int64_t)H * c->d.head_dim, dtype, q_stride, qs));
+    const long long rows = (long long)p->N * (H / p->H_kv);
+    if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
+    if (use_tc(dtype, rows) && tc_blocks(rows) * p->B * p->H_kv > (1 << 30))
+        return fail(ATLASKV_EUNSUPPORTED, "too many query rows for one call");
+    return ATLASKV_OK;
+}
+
 // Attention over the cache into a.out / a.lse or a.oseq / a.lse_seq.
 atlaskv_status attend_cache(atlaskv_cache *c, const atlaskv_seqs *seqs, int dtype, int H, float scale,
                             akv::CacheAttendIo a, void *workspace, size_t workspace_bytes, void *stream)
 {
-    AKV_RET(check_cache(c));
     akv::CacheParams p;
-    AKV_RET(cache_params(c, seqs, &p));
+    int64_t qs = 0;
     size_t need = 0;
-    AKV_RET(atlaskv_cache_workspace_size(c, dtype, seqs->B, seqs->N, H, &need));
-    if (!(scale >= 0.f) || std::isinf(scale)) return fail(ATLASKV_EINVAL, "scale must be finite and >= 0");
+    AKV_RET(check_attend(c, seqs, dtype, H, scale, a.q, a.qs, &p, &qs, &need));
     if (seqs->B == 0) return ATLASKV_OK;
     const int D = c->d.head_dim;
-    int64_t qs;
-    AKV_RET(check_rows("q", a.q, (int64_t)H * D, dtype, a.qs, &qs));
     if (!a.oseq && (!a.out || !aligned16(a.out))) return fail(ATLASKV_EINVAL, "null or unaligned out");
     if (a.lse && !aligned4(a.lse)) return fail(ATLASKV_EINVAL, "unaligned lse");
     if (!workspace || ((uintptr_t)workspace & 255u)) return fail(ATLASKV_EINVAL, "workspace must be 256-byte aligned");
@@ -302,7 +317,6 @@ atlaskv_status attend_cache(atlaskv_cache *c, const atlaskv_seqs *seqs, int dtyp
     a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
     a.ws = static_cast<uint8_t *>(workspace);
     const long long rows = (long long)p.N * a.G;
-    if (rows > (1 << 30)) return fail(ATLASKV_EUNSUPPORTED, "more than 2^30 query rows per KV head");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (use_tc(dtype, rows)) return D == 64 ? launch_tc<64>(c, p, a, s) : launch_tc<128>(c, p, a, s);
     return AKV_CA(dtype, D, row_tiles(dtype, rows), launch_ca, c, p, a, s);
@@ -551,6 +565,14 @@ atlaskv_status akv_cache_matches(const atlaskv_cache *c, int n_kv_heads, int hea
         return fail(ATLASKV_EINVAL, "the cache has %d KV heads of %d channels, the tree %d of %d", c->d.n_kv_heads,
                     c->d.head_dim, n_kv_heads, head_dim);
     return check_cache(c);
+}
+
+atlaskv_status akv_cache_check(const atlaskv_cache *c, const atlaskv_seqs *seqs, int dtype, int H, const void *q, float scale)
+{
+    akv::CacheParams p;
+    int64_t qs = 0;
+    size_t need = 0;
+    return check_attend(c, seqs, dtype, H, scale, q, 0, &p, &qs, &need);
 }
 
 atlaskv_status akv_cache_part(atlaskv_cache *c, const atlaskv_seqs *seqs, int dtype, int H, const void *q, float scale,

@@ -5,9 +5,10 @@ import pytest
 import torch
 
 from hierarchical_kv_pruning_b200 import binding
-from hierarchical_kv_pruning_b200.binding import AtlaskvError, KvCache, Rope
+from hierarchical_kv_pruning_b200.binding import AtlaskvError, HikvpTree, KvCache, Rope
 from tests import _cache_ref as ref
-from tests.test_gpu_cache import BF, F32, F64, check_attend, i32, new_cache, normal, tables
+from tests.test_gpu_cache import BF, F32, F64, check_attend, i32, new_cache, normal
+from tests.test_gpu_cache_tree import setup
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +219,38 @@ def test_stored_bytes_of_huge_and_tiny_groups(dtype):
             blk[code[t % 16, 32 * gr:32 * gr + 32:2]] = 0
             blk[sc[t % 16, 32 * gr]] = blk[sc[t % 16, 32 * gr] + 1] = 0
     assert torch.equal(got, want.bytes()), int((got != want.bytes()).sum())
+
+
+# ---- the whole attention with a cached sequence --------------------------------------
+
+@pytest.mark.parametrize("host", [None, 1])
+def test_attend_cached_refuses_before_it_starts(host):
+    """A refused call has written nothing, whatever it is refused for."""
+    w, cache, table, kv = setup(BF, 4, 2, 64, 2, [30, 45], 16, 5, host)
+    B, N, H, K = 2, 2, 4, w.shape.keep
+    with HikvpTree.from_workload(w) as tree, cache:
+        p = tree.params(K)
+        size = binding.atlaskv_workspace_size_cached(tree.handle, p, cache.handle, B, N, H)
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        out, kept = torch.full_like(w.q_seq, 7.0), [torch.full((B, H, k), -7, dtype=torch.int32, device="cuda") for k in K]
+        io = binding.atlaskv_io(B, N, H, N, w.q_kg.data_ptr(), w.q_seq.data_ptr(), None, None, out.data_ptr(), None,
+                                *[x.data_ptr() for x in kept])
+        seqs = lambda **kw: binding.atlaskv_seqs(*{**dict(B=B, N=N, max_pages=table.shape[1], block_table=table.data_ptr(),  # noqa: E731
+                                                          kv_len=kv.data_ptr(), q_len=None), **kw}.values())
+        for bad, status in ((dict(block_table=table.data_ptr() + 2), "EINVAL"), (dict(kv_len=kv.data_ptr() + 1), "EINVAL"),
+                            (dict(max_pages=1 << 27), "EUNSUPPORTED"), (dict(max_pages=0), "EINVAL"),
+                            (dict(block_table=None), "EINVAL"), (dict(kv_len=None), "EINVAL")):
+            with pytest.raises(AtlaskvError) as e:
+                binding.atlaskv_attend_cached(tree.handle, p, io, cache.handle, seqs(**bad), ws.data_ptr(), size)
+            assert e.value.status == getattr(binding, "ATLASKV_" + status)
+            torch.cuda.synchronize()
+            assert bool((out == 7.0).all()) and all(bool((x == -7).all()) for x in kept)
+        with pytest.raises(AtlaskvError):
+            binding.atlaskv_attend_cached(tree.handle, p, io, cache.handle, seqs(), ws.data_ptr(), size - 256)
+        torch.cuda.synchronize()
+        assert bool((out == 7.0).all()) and all(bool((x == -7).all()) for x in kept)
+        binding.atlaskv_attend_cached(tree.handle, p, io, cache.handle, seqs(), ws.data_ptr(), size,
+                                      torch.cuda.current_stream().cuda_stream)
+        tree.sync_status()
+        cache.sync_status()
+        assert all(bool((x >= 0).all()) for x in kept)
