@@ -144,8 +144,9 @@ struct atlaskv_tree {
     bool counting;                 // descent counters kept (ATLASKV_PROFILE_COUNTERS)
     bool timed;                    // the last attend recorded events
     bool counted;                  // the last attend kept descent counters
-    bool split;                    // bf16, D = 128: the sequence part runs on its own stream beside the descent
+    bool split;                    // bf16, host leaves: the sequence part runs on its own stream beside the descent
     bool host_mode_last;
+    bool seq_apart_last;           // the last timed attend's sequence part was a launch of its own
     int chunks_last;
     int num_sms;                   // of the device the tree was created on (grid sizing only)
     cudaEvent_t ev[kNumEvents];
@@ -1397,16 +1398,16 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
     // The sequence part depends only on the call's inputs: with the split it
     // starts at once on the tree's low-priority stream, beside the descent
     // (and the staging), and the leaf part merges with it afterwards.
-    auto cached_part = [&](cudaStream_t st) -> atlaskv_status {
-        return akv_cache_part(cs->cache, cs->seqs, t->d.dtype, io->H, io->q_seq, ks.scale, ap.oseq, ap.lse_seq,
-                              ws + L.total, cs->ws_bytes, st);
+    auto timed_cached_part = [&](cudaStream_t st) -> atlaskv_status {
+        AKV_STEP(tm(2, st));
+        AKV_STEP(akv_cache_part(cs->cache, cs->seqs, t->d.dtype, io->H, io->q_seq, ks.scale, ap.oseq, ap.lse_seq,
+                                ws + L.total, cs->ws_bytes, st));
+        return tm(3, st);
     };
     auto fork_sequence_part = [&]() -> atlaskv_status {
         AKV_CUDA(cudaStreamWaitEvent(t->seq_stream, t->fev[0], 0));
         if (cs) {
-            AKV_STEP(tm(2, t->seq_stream));
-            AKV_STEP(cached_part(t->seq_stream));
-            AKV_STEP(tm(3, t->seq_stream));
+            AKV_STEP(timed_cached_part(t->seq_stream));
             AKV_CUDA(cudaEventRecord(t->fev[2], t->seq_stream));
             return ATLASKV_OK;
         }
@@ -1445,7 +1446,7 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
             AKV_STEP(tm(5, s));
         } else {
             if (cs) {
-                AKV_STEP(cached_part(s));
+                AKV_STEP(timed_cached_part(s));
                 ap.mode = akv::kAttnLeaf;
             }
             AKV_STEP(tm(0, s));
@@ -1570,7 +1571,7 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
             AKV_CUDA(cudaEventRecord(t->fev[0], s));
             AKV_STEP(fork_sequence_part());
         } else if (cs) {
-            AKV_STEP(cached_part(s));
+            AKV_STEP(timed_cached_part(s));
         }
         if (t->cache_pool) ++t->cache_epoch;   // this call's stamp (epoch 0 marks empty ways)
         for (int k = 0; k < np; ++k) {
@@ -1626,6 +1627,7 @@ atlaskv_status attend_impl(atlaskv_tree *t, const Ks &ks, const atlaskv_io *io, 
     t->timed = prof;
     t->counted = t->counting;
     t->host_mode_last = host;
+    t->seq_apart_last = t->split || cs;
     return ATLASKV_OK;
 }
 
@@ -1834,6 +1836,7 @@ atlaskv_status atlaskv_attend_layers(int32_t n_layers, atlaskv_tree *const *tree
         trees[l]->timed = l == 0 && prof;
         trees[l]->counted = trees[l]->counting;
         trees[l]->host_mode_last = false;
+        trees[l]->seq_apart_last = trees[l]->split;
     }
     return ATLASKV_OK;
 }
@@ -1951,7 +1954,7 @@ atlaskv_status atlaskv_stage_times(atlaskv_tree *t, float *ms, int32_t n)
                 v[kind == kPhaseDescend ? 0 : kind == kPhaseAttend ? 4 : 1] += seg;
             }
     }
-    if (t->split) AKV_CUDA(cudaEventElapsedTime(&v[3], t->ev[2], t->ev[3]));
+    if (t->seq_apart_last) AKV_CUDA(cudaEventElapsedTime(&v[3], t->ev[2], t->ev[3]));
     v[2] = v[3] + v[4];
     for (int i = 0; i < n && i < 5; ++i) ms[i] = v[i];
     return ATLASKV_OK;

@@ -294,8 +294,9 @@ atlaskv_status atlaskv_set_descent(atlaskv_tree *tree, int32_t mode);
 /* Per-stage device times (ms) of the most recent attend call made with
  * ATLASKV_PROFILE_TIMES: [0] descent levels, [1] host-leaf staging (0 when
  * leaves are in HBM), [2] attention + merge ([3] + [4]), [3] the sequence
- * part when it runs as its own launch (bf16, D = 128; else 0), [4] the leaf
- * part (or the whole attention when it is one launch).  With host leaves
+ * part when it runs as its own launches (host leaves in bf16, or a cached
+ * sequence; else 0), [4] the leaf part (or the whole attention when it is one
+ * launch).  With host leaves
  * [0], [1] and [4] are busy times summed over the query chunks.  Synchronises
  * the stream of that call.  n is the capacity of ms (at most 5 written);
  * returns EINVAL if that call recorded no times. */

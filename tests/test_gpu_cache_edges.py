@@ -254,3 +254,17 @@ def test_attend_cached_refuses_before_it_starts(host):
         tree.sync_status()
         cache.sync_status()
         assert all(bool((x >= 0).all()) for x in kept)
+
+
+@pytest.mark.parametrize("dtype,host", [(BF, None), (F32, None), (BF, 1), (F32, 1)])
+def test_stage_times_hold_the_cached_sequence_part(dtype, host):
+    w, cache, table, kv = setup(dtype, 4, 2, 64, 2, [300, 45], 16, 5, host)
+    with HikvpTree.from_workload(w) as tree, cache:
+        binding.atlaskv_set_profiling(tree.handle, binding.ATLASKV_PROFILE_TIMES)
+        tree.attend_cached(w.q_kg, w.q_seq, cache, table, kv, w.shape.keep)
+        ms = binding.atlaskv_stage_times(tree.handle)
+        assert ms[3] > 0 and ms[4] > 0 and ms[2] == pytest.approx(ms[3] + ms[4], rel=1e-5)
+        k, v = cache.read(300, table, kv, kv, dtype=dtype)
+        tree.attend(w.q_kg, w.q_seq, k, v, w.shape.keep)          # an earlier call's time does not stay
+        ms = binding.atlaskv_stage_times(tree.handle)
+        assert (ms[3] > 0) == (dtype == BF and host is not None)
