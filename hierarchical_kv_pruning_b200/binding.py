@@ -756,7 +756,17 @@ class Rope:
 def rope(x, positions, spec: Rope, out=None, backward: bool = False, stream=None):
     """Rotate x [B][N][H][D] by positions [B][N] (int32) into out (a new
     tensor by default; x itself for in place).  backward=True is the transpose:
-    it turns a gradient of the rotated tensor into that of the tensor."""
+    it turns a gradient of the rotated tensor into that of the tensor.  An x
+    that requires a gradient gets it so in autograd, on the stream that is
+    current; not with out=, which is refused unless gradients are off."""
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise AtlaskvError(ATLASKV_EINVAL, "rope(out=) records no gradient, and x requires one")
+        return _Rotation.apply(x, positions, spec, backward, stream)
+    return _rotate(x, positions, spec, out, backward, stream)
+
+
+def _rotate(x, positions, spec: Rope, out, backward: bool, stream):
     shape, dtype, new = x.shape, x.dtype, ()
     if len(shape) != 4 or not x.is_cuda:
         raise AtlaskvError(ATLASKV_EINVAL, "x must be a CUDA tensor [B][N][H][D]")
@@ -773,13 +783,27 @@ def rope(x, positions, spec: Rope, out=None, backward: bool = False, stream=None
     return out
 
 
+class _Rotation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, spec, backward, stream):
+        ctx.save_for_backward(positions)
+        ctx.spec, ctx.direction = spec, bool(backward)
+        return _rotate(x, positions, spec, None, backward, stream)
+
+    @staticmethod
+    def backward(ctx, dy):
+        positions, = ctx.saved_tensors
+        # (a gradient may be expanded; one that a second pass needs is recorded in its turn)
+        return rope(dy.contiguous(), positions, ctx.spec, backward=not ctx.direction), None, None, None, None
+
+
 class KvCache:
     """A pool of 4-bit cache pages registered with the library.  pages: uint8
     [n_pages][page bytes] on the GPU (KvCache.page_bytes gives the width),
     borrowed and kept alive.  The calls take one batch's block_table
     [B][max_pages], kv_len [B] and q_len [B] (or None: every row), int32 on the
     GPU, as atlaskv_seqs describes them; a decode step appends its tokens and
-    attends with the same three."""
+    attends with the same three.  For serving: no call records a gradient."""
 
     def __init__(self, pages, n_kv_heads: int, head_dim: int, page_size: int, stream=None):
         self.handle = None

@@ -268,3 +268,60 @@ def test_stage_times_hold_the_cached_sequence_part(dtype, host):
         tree.attend(w.q_kg, w.q_seq, k, v, w.shape.keep)          # an earlier call's time does not stay
         ms = binding.atlaskv_stage_times(tree.handle)
         assert (ms[3] > 0) == (dtype == BF and host is not None)
+
+
+# ---- the rotation's gradient --------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_records_its_gradient(dtype, inter):
+    """A tensor that requires a gradient gets the transpose's, and the transpose of that the rotation's."""
+    spec, pos = Rope(48, interleaved=inter, amplitude=1.3), i32([[0, 3, 70000], [12, 9, 1 << 20]])
+    x, g, gg = (normal(s, 2, 3, 2, 64, dtype=dtype).cuda() for s in (1, 2, 3))
+    for back in (False, True):
+        leaf = x.clone().requires_grad_()
+        y = binding.rope(leaf, pos, spec, backward=back)
+        assert y.requires_grad and torch.equal(y, binding.rope(x, pos, spec, backward=back))
+        up = g.clone().requires_grad_()
+        d, = torch.autograd.grad(y, leaf, up, create_graph=True)
+        assert torch.equal(d, binding.rope(g, pos, spec, backward=not back))
+        dd, = torch.autograd.grad(d, up, gg)
+        assert torch.equal(dd, binding.rope(gg, pos, spec, backward=back))
+        with torch.no_grad():
+            assert not binding.rope(leaf, pos, spec, backward=back).requires_grad
+        # a gradient that is expanded, as a sum's is
+        s, = torch.autograd.grad(binding.rope(leaf, pos, spec, backward=back).sum(), leaf)
+        assert torch.equal(s, binding.rope(torch.ones_like(x), pos, spec, backward=not back))
+
+
+def test_rope_gradient_through_a_wider_projection():
+    """A slice of a projection, on another stream, in a captured step."""
+    spec, pos = Rope(64), i32([[0, 3, 70000], [12, 9, 1 << 20]])
+    wide = normal(4, 2, 3, 6, 128, dtype=BF).cuda().requires_grad_()
+    g = normal(5, 2, 3, 4, 128, dtype=BF).cuda()
+    want = torch.zeros_like(wide)
+    want[:, :, 1:5] = binding.rope(g, pos, spec, backward=True)
+
+    def step():
+        return torch.autograd.grad(binding.rope(wide[:, :, 1:5], pos, spec), wide, g)[0]
+    assert torch.equal(step(), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step()
+        graph.replay()
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_rope_out_refuses_to_lose_a_gradient():
+    spec, pos = Rope(64), i32([[0, 1, 2], [3, 4, 5]])
+    x = normal(1, 2, 3, 4, 64, dtype=BF).cuda().requires_grad_()
+    with pytest.raises(AtlaskvError) as e:
+        binding.rope(x, pos, spec, out=torch.empty_like(x))
+    assert e.value.status == binding.ATLASKV_EINVAL
+    with torch.no_grad():
+        assert torch.equal(binding.rope(x, pos, spec, out=torch.empty_like(x)), binding.rope(x, pos, spec))
