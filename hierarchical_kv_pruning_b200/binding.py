@@ -534,7 +534,7 @@ class HikvpTree:
                         *[_ints("kept", x, (B, H, int(k))) for x, k in zip(kept, K)])
         seqs = cache._seqs(B, N, block_table, kv_len, None)
         _used_on(stream, *new)
-        atlaskv_attend_cached(self.handle, p, io, cache.handle, seqs, workspace.data_ptr(), workspace.nbytes, s)
+        atlaskv_attend_cached(self.handle, p, io, cache.handle, seqs, *_space(workspace), s)
         return {"out": out, "lse": lse, "kept_root": kept[0], "kept_mid": kept[1], "kept_leaf": kept[2],
                 "workspace": workspace}
 
@@ -717,6 +717,14 @@ def _dense(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> int:
 
 def _ints(name: str, t: Optional[torch.Tensor], shape) -> Optional[int]:
     return None if t is None else _dense(name, t, shape, torch.int32)
+
+
+def _space(t: torch.Tensor):
+    """(address, bytes) of a workspace: its own bytes, all of them, and no others."""
+    if not t.is_contiguous():
+        raise AtlaskvError(ATLASKV_EINVAL, "the workspace must be contiguous, not of shape %s and strides %s" %
+                           (tuple(t.shape), t.stride()))
+    return t.data_ptr(), t.nbytes
 
 
 def _on_device(index: int, stream, *tensors) -> int:
@@ -925,7 +933,7 @@ class KvCache:
                                      scale)
         seqs = self._seqs(B, N, block_table, kv_len, q_len)
         _used_on(stream, *new)
-        atlaskv_cache_attend(self.handle, seqs, io, workspace.data_ptr(), workspace.nbytes, s)
+        atlaskv_cache_attend(self.handle, seqs, io, *_space(workspace), s)
         return out, lse
 
     def sync_status(self, stream=None):

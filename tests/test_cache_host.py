@@ -188,3 +188,14 @@ def test_rows_takes_slices_of_wider_rows():
     one = wide[:1, :1, :4].expand(1, 1, 4, 128)
     assert binding._rows("x", one, torch.Size((1, 1, 4, 128)), torch.float32) in (0, 4 * 128)
     assert binding._rows("x", wide[:0, :, :4], torch.Size((0, 5, 4, 128)), torch.float32) == 0
+
+
+def test_workspaces_are_their_own_bytes():
+    """A workspace whose bytes repeat or skip memory would be written past, or between, them."""
+    ws = torch.empty(1024, dtype=torch.uint8)
+    assert binding._space(ws) == (ws.data_ptr(), 1024) and binding._space(ws[256:])[1] == 768
+    assert binding._space(ws.view(torch.float32))[1] == 1024
+    for bad in (ws[:1].expand(1 << 30), ws[::2], ws.view(32, 32)[:, :16]):
+        with pytest.raises(binding.AtlaskvError) as e:
+            binding._space(bad)
+        assert e.value.status == binding.ATLASKV_EINVAL

@@ -325,3 +325,14 @@ def test_rope_out_refuses_to_lose_a_gradient():
     assert e.value.status == binding.ATLASKV_EINVAL
     with torch.no_grad():
         assert torch.equal(binding.rope(x, pos, spec, out=torch.empty_like(x)), binding.rope(x, pos, spec))
+
+
+def test_expanded_workspaces_are_refused():
+    w, cache, table, kv = setup(BF, 4, 2, 64, 2, [30, 45], 16, 5)
+    bad = torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 30)
+    with HikvpTree.from_workload(w) as tree, cache:
+        for call in (lambda: cache.attend(w.q_seq, table, kv, workspace=bad),
+                     lambda: tree.attend_cached(w.q_kg, w.q_seq, cache, table, kv, w.shape.keep, workspace=bad)):
+            with pytest.raises(AtlaskvError) as e:
+                call()
+            assert e.value.status == binding.ATLASKV_EINVAL
