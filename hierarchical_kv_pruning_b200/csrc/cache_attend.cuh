@@ -59,6 +59,18 @@ __device__ __forceinline__ void ca_write(const CacheParams &c, const CacheAttend
 // registers a thread, so two CTAs an SM, bound it.  One sequence of 513 tokens: 10 us,
 // a chain of the plan, the table, a copy and five rounds of units (1 us each).
 //
+// Rounding: logits, maxima, sums and O are float32.  A bfloat16 call's
+// probabilities are rounded to bfloat16 for their product with V (2^-9 each, as in
+// the dense sequence attention; O is rounded as much at the end, and a second
+// part would double that product), the sum l takes them unrounded; a float32
+// call's are three bfloat16 parts, exact to 2^-24.  The matrix unit's sums are cut,
+// not rounded, which a bfloat16 call does not feel; a float32 call's sums over a
+// step of 32 channels or of 16 tokens are taken from 0 and added to the running
+// ones by rounded additions.  With one running sum all the way, outputs over 16000
+// tokens were 9e-6 too small; now they are 1.6e-7 too small and off by 4e-7 of their
+// norm, for 2 to 9 % more time (512 x 16 rows of 128 or 64 channels over 16000
+// tokens: 616 -> 628, 363 -> 395 us).
+//
 // The products run on m16n8k16 with the cache as the 16-row operand, S^T = K
 // Q^T and O^T = V^T P^T: a decode step has few rows, so they take the 8-wide
 // side (tcgen05 has 128-row operands only, and its operands go through shared
@@ -149,6 +161,15 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, const uint
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ void add4(float *d, const float *a)
+{
+    const float2 x = add2(make_float2(d[0], d[1]), make_float2(a[0], a[1])), y = add2(make_float2(d[2], d[3]), make_float2(a[2], a[3]));
+    d[0] = x.x;
+    d[1] = x.y;
+    d[2] = y.x;
+    d[3] = y.y;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
@@ -499,6 +520,15 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) stored8(w[k][h][x], ks[k][h], n[k][h]);
+                float part[2][NT][4];   // this step's, of float32 queries
+                if constexpr (P > 1) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) part[k][j][e] = 0.f;
+                }
 #pragma unroll
                 for (int y = 0; y < 2; ++y)   // contraction step 2 x + y
 #pragma unroll
@@ -518,9 +548,15 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                             for (int k = 0; k < 2; ++k) {
                                 const uint32_t a[4] = {n[k][0][2 * y], n[k][1][2 * y], n[k][0][2 * y + 1],
                                                        n[k][1][2 * y + 1]};
-                                mma16816(sc[k][j], a, bq);
+                                mma16816(P > 1 ? part[k][j] : sc[k][j], a, bq);
                             }
                         }
+                if constexpr (P > 1) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) add4(sc[k][j], part[k][j]);
+                }
             }
 
             // ---- softmax: element (token r + 8 (e / 2), row 2 t + (e & 1)) ----
@@ -624,9 +660,12 @@ __global__ void __launch_bounds__(kCaThreads, Ca<T, D, NT>::kCtas)
                         const int d = 2 * y + e;
                         const uint32_t a[4] = {n0[2 * e], n0[2 * e + 1], n1[2 * e], n1[2 * e + 1]};
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
+                        for (int j = 0; j < NT; ++j) {
+                            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) mma16816(acc[j][d], a, pf[p][j][k]);
+                            for (int p = 0; p < P; ++p) mma16816(P > 1 ? part : acc[j][d], a, pf[p][j][k]);
+                            if constexpr (P > 1) add4(acc[j][d], part);
+                        }
                     }
                 }
             }

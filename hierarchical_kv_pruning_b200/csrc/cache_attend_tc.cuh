@@ -14,7 +14,9 @@
 //                   is stored in the same order, O is put back in the epilogue;
 //   2 MMA warps     S = Q K^T (M 128, N 64) of the next key tile for both row
 //                   tiles, and O += P V, P read from TMEM where it overlays S;
-//   2 x 4 warps     softmax, one thread per row: as in the few-rows kernel.
+//   2 x 4 warps     softmax, one thread per row, roundings as in the few-rows
+//                   kernel: P is bfloat16, because the product takes its two
+//                   operands in one type and V is; everything else float32.
 // TMEM: S / P 2 x 2 x 64 and O 2 x D columns.  Shared memory (D = 128): Q 64, K
 // 48, V 48, codes 40 KB.
 // What bounds it: per key tile and both row tiles (D = 128) the products take

@@ -139,7 +139,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v)
 }
 
 // 2^x with the MUFU approximation (ex2.approx.ftz: relative error about
-// 2^-22, 2^-inf = 0); the probabilities are rounded to bf16 afterwards.
+// 2^-22, 2^-inf = 0): bf16 probabilities lose 2^-9 afterwards, and three-part
+// ones keep what this gives.
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;

@@ -336,3 +336,23 @@ def test_expanded_workspaces_are_refused():
             with pytest.raises(AtlaskvError) as e:
                 call()
             assert e.value.status == binding.ATLASKV_EINVAL
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_float32_outputs_do_not_shrink_with_the_length(D):
+    """The matrix unit cuts its sums, so a running sum over thousands of steps comes out too small.  The share by which
+    the outputs are, sum (y - o) o / sum o^2, is at most 3 cut steps of a 16-token sum (2^-23 each) and 6 of a
+    32-channel logit, whose shrinking moves outputs by no more than that times the logits' spread of 1.5: 12 2^-23.  The
+    roundings of 16 D outputs average out below 2^-24, of which three times as much is allowed: 13.5 2^-23."""
+    n, B, N, H, P = 16000, 600, 2, 8, 64
+    pool = ref.Pool(n // P, 1, D, P)
+    table = torch.arange(n // P, dtype=torch.int32).repeat(B, 1)       # enough equal sequences that a CTA takes whole ones
+    pool.fill(table[0], n, 3)
+    q = normal(71, 1, N, H, D)
+    with new_cache(pool) as cache:
+        out, _ = cache.attend(q.repeat(B, 1, 1, 1).cuda(), table.cuda(), i32([n] * B))
+        cache.sync_status()
+    k, v = pool.all(table[0], n)
+    o = ref.attend(q[0].to(F64), k, v, N)[0].cuda()
+    share = ((out.double() - o) * o).sum((1, 2, 3)) / (o * o).sum()
+    assert float(share.abs().max()) <= 13.5 * 2.0 ** -23, (float(share.min()), float(share.max()))
