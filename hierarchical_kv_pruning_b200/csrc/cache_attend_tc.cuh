@@ -28,7 +28,8 @@
 // products), 64-token tiles with two S buffers and one issuing warp 7400, products
 // issued under elect.sync instead of one lane's branch 6200, S and P V issued by a
 // warp each 5200, the maximum searched only where it must grow 5000.  2 x 2048 tokens over
-// 6k .. 8k, 32 heads on 8 (390 GFLOP): 495 us with the join, 0.79 PFLOP/s.
+// 6k .. 8k, 32 heads on 8 (390 GFLOP): 515 us with the join, 0.76 PFLOP/s.  96
+// registers a thread at launch leave 308 bytes of spills, 324 at D = 64.
 //
 // The runs of units per CTA are as in the few-rows kernel, unless whole items
 // balance about as well (a partial of 256 rows costs as much as several tiles).

@@ -224,7 +224,8 @@ __device__ __forceinline__ double rotated64(const RopeParams &p, const T *row, i
 // rows as they are), decided in float64 from the rows
 // themselves, a channel per lane: what is stored does not depend on float32's
 // roundings, nor on float64's: the scale rounds up at each step, and a tie is broken
-// by what x - m lost.  5.3k tokens take 2 us more.  All lanes of a warp call it, with
+// by what x - m lost.  5.3k tokens take 1 us more, half of that with queries beside
+// them.  All lanes of a warp call it, with
 // what quantise16 gave them: lane l of a row holds channels 16 l .. 16 l + 15.
 template <typename T>
 __device__ __forceinline__ void settle(const RopeParams &p, bool doubt, const T *row, int l, int pos, bool rotate,
@@ -323,8 +324,8 @@ struct AppendIo {
 // queries', but the rounding to codes, about 15 instructions a number, takes
 // as long: side by side the one's memory time hides the other's issue slots
 // (the same CTA doing one after the other measured 51 us where this took 34,
-// 5.3k tokens of 32 + 2 x 8 heads; with settle it takes 37, 2.5 TB/s: the issue
-// slots, 2.5 instructions a cycle, bound it, not HBM).
+// 5.3k tokens of 32 + 2 x 8 heads; with settle and exact scales it takes 37.6, 2.5
+// TB/s: the issue slots, 2.6 instructions a cycle, bound it, not HBM).
 template <typename T, int D>
 __global__ void __launch_bounds__(kTokThreads, 4)
     cache_append_kernel(const __grid_constant__ RopeParams p, const CacheParams c, const AppendIo io)
